@@ -1,10 +1,11 @@
 """Python binding of libsplitzip.so, the gfx950 lossless exponent codec for
 BF16 and FP8-E5M2 KV-cache tensors (SplitZip project page, "Abstract"), and
 of the LC-style comparison codec in the same library (FastKVComp companion
-page, "Inside an LC-style pipeline").
+page, "Inside an LC-style pipeline"), and of the paged KV cache that the
+coded layer tensors come from and go to (append, attention, gather, scatter).
 
-Thin ctypes marshalling over the C ABI declared in include/splitzip.h and
-include/lc_codec.h: the functions below carry the C names and arguments.  Pointer arguments accept
+Thin ctypes marshalling over the C ABI declared in include/splitzip.h,
+include/lc_codec.h and include/paged_kv.h: the functions below carry the C names and arguments.  Pointer arguments accept
 a torch tensor (its data_ptr()), a plain integer address or None; `stream`
 defaults to torch's current stream.  torch provides device memory and
 streams only -- every step of the codec runs in the library's HIP kernels.
@@ -30,6 +31,8 @@ __all__ = [
     "sz_status_string", "check", "pointer_table", "library_path",
     "lc_max_compressed_bytes", "lc_encode_workspace_bytes", "lc_encode_workspace_bytes_batched",
     "lc_encode", "lc_decode", "lc_encode_batched", "lc_decode_batched",
+    "KvCache", "KvBatch", "KvAppendArgs", "KvAttentionArgs",
+    "kv_append", "kv_attention_workspace_bytes", "kv_attention", "kv_gather", "kv_scatter",
 ]
 
 SZ_DTYPE_BF16 = 1
@@ -43,6 +46,7 @@ SZ_ERR_TIMEOUT = 5
 SZ_NOALLOC_MAX_ELEMENTS = 1 << 24                  # include/splitzip.h
 SZ_NOALLOC_SCRATCH_BYTES = (16 << 20) + (64 << 10)
 SZ_ABI_VERSION = 4                                 # include/splitzip.h: the signatures below are for it
+KV_ABI_VERSION = 1                                 # include/paged_kv.h, likewise
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsplitzip.so")
@@ -81,6 +85,12 @@ _SIGNATURES = {
     "lc_decode": (_i32, [_vp, _u64, _u64, _vp, _vp, _vp]),
     "lc_encode_batched": (_i32, [_vp, _u32, _u64, _vp, _u64, _vp, _vp, _u64, _vp]),
     "lc_decode_batched": (_i32, [_vp, _vp, _u32, _u64, _vp, _vp, _vp]),
+    "kv_append": (_i32, [_vp, _vp, _vp, _vp, _vp]),
+    "kv_attention_workspace_bytes": (_u64, [_vp, _vp, _vp]),
+    "kv_attention": (_i32, [_vp, _vp, _vp, _vp, _u64, _vp, _vp]),
+    "kv_gather": (_i32, [_vp, _vp, _vp, _u64, _vp, _u64, _vp, _vp]),
+    "kv_scatter": (_i32, [_vp, _vp, _vp, _u64, _vp, _u64, _vp, _vp]),
+    "kv_abi_version": (_u32, []),
 }
 if not hasattr(_lib, "sz_abi_version"):
     raise ImportError(f"{_LIB_PATH} predates the ABI version check; rebuild it")
@@ -89,6 +99,12 @@ if _lib.sz_abi_version() != SZ_ABI_VERSION:
     # a library from another revision: its signatures may not be the ones below
     raise ImportError(f"{_LIB_PATH} has ABI version {_lib.sz_abi_version()}, this binding wants "
                       f"{SZ_ABI_VERSION}; rebuild it")
+if not hasattr(_lib, "kv_abi_version"):
+    raise ImportError(f"{_LIB_PATH} predates the paged KV cache; rebuild it")
+_lib.kv_abi_version.restype = _u32
+if _lib.kv_abi_version() != KV_ABI_VERSION:
+    raise ImportError(f"{_LIB_PATH} has paged-cache ABI version {_lib.kv_abi_version()}, this binding wants "
+                      f"{KV_ABI_VERSION}; rebuild it")
 for _name, (_res, _args) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
     _fn.restype = _res
@@ -273,3 +289,54 @@ def lc_encode_batched(srcs, count, n, dsts, dst_capacity, out_bytes, workspace, 
 def lc_decode_batched(srcs, src_bytes, count, n, dsts, status=None, stream=None):
     return _lib.lc_decode_batched(_ptr(srcs), _ptr(src_bytes), count, n, _ptr(dsts), _ptr(status),
                                   _stream(stream))
+
+
+class KvCache(ctypes.Structure):
+    """kv_cache: one layer's key and value pools."""
+    _fields_ = [("d_k", _vp), ("d_v", _vp), ("page_stride", _u64), ("token_stride", _u64), ("head_stride", _u64),
+                ("num_pages", _u32), ("page_size", _u32), ("kv_heads", _u32), ("head_dim", _u32), ("dtype", _i32),
+                ("reserved", _u32)]
+
+
+class KvBatch(ctypes.Structure):
+    """kv_batch: a step's sequences, their pages and lengths."""
+    _fields_ = [("d_pages", _vp), ("d_cu_tokens", _vp), ("d_kv_lens", _vp), ("pages_stride", _u64),
+                ("pages_per_seq", _u32), ("num_seqs", _u32), ("total_tokens", _u32), ("max_tokens", _u32),
+                ("max_kv_len", _u32), ("reserved", _u32)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """kv_append_args."""
+    _fields_ = [("d_k", _vp), ("d_v", _vp), ("d_q", _vp), ("d_q_out", _vp), ("k_stride", _u64), ("v_stride", _u64),
+                ("q_stride", _u64), ("q_out_stride", _u64), ("d_cos_sin", _vp), ("d_q_norm", _vp),
+                ("d_k_norm", _vp), ("eps", ctypes.c_float), ("q_heads", _u32), ("rotary_dim", _u32),
+                ("max_positions", _u32), ("interleaved", _u32), ("reserved", _u32)]
+
+
+class KvAttentionArgs(ctypes.Structure):
+    """kv_attention_args."""
+    _fields_ = [("d_q", _vp), ("d_out", _vp), ("d_lse", _vp), ("q_stride", _u64), ("out_stride", _u64),
+                ("scale", ctypes.c_float), ("q_heads", _u32), ("causal", _u32), ("window", _u32)]
+
+
+def kv_append(cache, batch, args, status=None, stream=None):
+    return _lib.kv_append(_opts(cache), _opts(batch), _opts(args), _ptr(status), _stream(stream))
+
+
+def kv_attention_workspace_bytes(cache, batch, args):
+    return _lib.kv_attention_workspace_bytes(_opts(cache), _opts(batch), _opts(args))
+
+
+def kv_attention(cache, batch, args, workspace, workspace_bytes, status=None, stream=None):
+    return _lib.kv_attention(_opts(cache), _opts(batch), _opts(args), _ptr(workspace), workspace_bytes, _ptr(status),
+                             _stream(stream))
+
+
+def kv_gather(cache, batch, k, k_stride, v, v_stride, status=None, stream=None):
+    return _lib.kv_gather(_opts(cache), _opts(batch), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(status),
+                          _stream(stream))
+
+
+def kv_scatter(cache, batch, k, k_stride, v, v_stride, status=None, stream=None):
+    return _lib.kv_scatter(_opts(cache), _opts(batch), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(status),
+                           _stream(stream))

@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsplitzip.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "api.cpp", "lc_kernels.hip", "lc_api.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "api.cpp", "lc_kernels.hip", "lc_api.cpp",
+                                           "kv_kernels.hip", "kv_attention.hip", "kv_api.cpp")]
 PROBE_LIB = os.path.join(HERE, "libszprobe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "probe.hip")]
 ARCH = "gfx950"

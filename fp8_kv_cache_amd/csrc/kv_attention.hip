@@ -1,0 +1,563 @@
+// kv_attention.hip -- attention of new tokens over the paged KV cache
+// (include/paged_kv.h, kv_attention).
+//
+// Mathematics.  For the rows of one sequence under one KV head, with
+// c = scale * log2(e):  s_j = q . k_j,  m = max_j c s_j,
+// p_j = 2^(c s_j - m),  o = sum_j p_j v_j / sum_j p_j, in one pass over the
+// keys: when a block raises m, the sums so far are multiplied by
+// 2^(m_old - m).  lse = (m + log2 sum) ln 2.
+//
+// Layout.  Both products run transposed on the matrix cores, S^T = K Q^T and
+// O^T = V^T P^T, so that a lane holds one query row (column of S^T and O^T):
+// the row's maximum and sum are kept in that lane, its rescaling multiplies
+// that lane's registers, and S^T's result layout is P^T's operand layout once
+// the keys of the second product are numbered to fit it (any numbering will
+// do as long as V^T has the same).  V^T's operand has the keys along a
+// lane's registers: V is staged row-major in LDS and read with the
+// transposing 4 x 16 LDS read.
+//
+// E5M2 is the upper byte of FP16, so an E5M2 cache is expanded by byte
+// permutes and multiplied in FP16.  The query row is scaled by a power of
+// two that brings its largest element to [2^14, 2^15) before it becomes FP16
+// (and c by its inverse): elements down to 2^-28 of the largest keep all of
+// BF16's bits, smaller ones lose less than 2^-38 of the largest.
+#include "kv_internal.h"
+
+#include "device_common.h"
+#include "splitzip.h"
+
+namespace kvi {
+
+namespace {
+
+using sz::gptr;
+using sz::u32x2;
+using sz::u32x4;
+using sz::uniform;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_inff();
+
+__device__ inline void flag(int32_t* status) {
+    if (status) *gptr(status) = SZ_ERR_INVALID_ARGUMENT;
+}
+
+__device__ inline f32x8 to_f32(u32x4 x) { return __builtin_convertvector(__builtin_bit_cast(bf16x8, x), f32x8); }
+
+// 8 E5M2 bytes -> 8 FP16
+__device__ inline u32x4 expand(u32x2 b) {
+    return u32x4{sz::perm(0, b[0], 0x010C000Cu), sz::perm(0, b[0], 0x030C020Cu), sz::perm(0, b[1], 0x010C000Cu),
+                 sz::perm(0, b[1], 0x030C020Cu)};
+}
+
+template <bool kE5M2>
+__device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (kE5M2)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool kE5M2>
+__device__ inline u32x4 pack(f32x8 x) {   // to the matrix cores' 16-bit type, nearest even
+    if constexpr (kE5M2) return __builtin_bit_cast(u32x4, __builtin_convertvector(x, f16x8));
+    else return __builtin_bit_cast(u32x4, __builtin_convertvector(x, bf16x8));
+}
+
+// max or sum over the lanes that hold the same query row (lane, lane ^ 16, lane ^ 32, lane ^ 48)
+__device__ inline float swap16(float x, bool hi) {
+    const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(hi ? r[1] : r[0]);
+}
+__device__ inline float swap32(float x, bool hi) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(hi ? r[1] : r[0]);
+}
+__device__ inline float row_max(float x) {
+    x = fmaxf(swap16(x, false), swap16(x, true));
+    return fmaxf(swap32(x, false), swap32(x, true));
+}
+__device__ inline float row_sum(float x) {
+    x = swap16(x, false) + swap16(x, true);
+    return swap32(x, false) + swap32(x, true);
+}
+
+// Whether any of 8 packed 16-bit values is Inf or NaN.
+template <bool kE5M2>
+__device__ inline bool not_finite(u32x4 x) {
+    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        any |= (x[i] & kExp) == kExp || (x[i] & (kExp << 16)) == (kExp << 16);
+    return any;
+}
+
+// Splits 8 packed values into the finite ones (others 0) and markers (1.0)
+// of those that bring +Inf (+Inf, NaN) and -Inf (-Inf, NaN) into a sum.
+template <bool kE5M2>
+__device__ inline void part_values(u32x4& x, u32x4& up, u32x4& down) {
+    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u, kOne = kE5M2 ? 0x3C00u : 0x3F80u;
+    up = down = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            const uint32_t v = (x[i] >> h) & 0xFFFFu;
+            if ((v & kExp) != kExp) continue;
+            const bool nan = (v & (0x7FFFu & ~kExp)) != 0, minus = v >> 15;
+            if (nan || !minus) up[i] |= kOne << h;
+            if (nan || minus) down[i] |= kOne << h;
+            x[i] &= ~(0xFFFFu << h);
+        }
+}
+
+// Accumulates V^T P^T where the rows of a tile see different keys and V
+// holds Inf or NaN: a weight of 0 would not keep them out of the product.
+// Their markers meet the mask instead of the weights, and a row that sees
+// one gets it added.
+template <bool kE5M2, typename F, typename Acc>
+__device__ inline Acc add_marked(F mfma, u32x4 v, u32x4 p, u32x4 seen, Acc o) {
+    u32x4 up, down;
+    part_values<kE5M2>(v, up, down);
+    o = mfma(v, p, o);
+    Acc a{}, b{};
+    a = mfma(up, seen, a);
+    b = mfma(down, seen, b);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Acc) / 4); ++i) {
+        if (a[i] > 0.f) o[i] += kInf;
+        if (b[i] > 0.f) o[i] -= kInf;
+    }
+    return o;
+}
+
+template <bool kE5M2>
+struct Mfma16 {
+    __device__ f32x4 operator()(u32x4 a, u32x4 b, f32x4 c) const { return mfma16<kE5M2>(a, b, c); }
+};
+
+// LDS order inside one wave: its LDS instructions execute in order; this
+// keeps the compiler from moving one lane's reads over another's writes.
+__device__ inline void wave_lds_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Query row `row` of the tile's sequence: its token and head.
+struct RowAt {
+    uint32_t token;   // row of the per-token tensors
+    uint32_t head;
+    int32_t p;
+};
+__device__ inline RowAt row_at(const Tile& t, uint32_t row, uint32_t group, uint32_t kv_head) {
+    const uint32_t i = row / group;
+    return RowAt{static_cast<uint32_t>(t.seq.begin) + i, kv_head * group + (row - i * group),
+                 t.seq.first() + static_cast<int32_t>(i)};
+}
+
+// Writes one row's share: the output where the tile has one split, else the
+// sums for k_join.  `put(d, x4)` style stores are done by the callers.
+__device__ inline void put_lse(const AttentionArgs& a, const RowAt& r, float m, float l) {
+    if (a.lse)
+        gptr(a.lse)[static_cast<uint64_t>(r.token) * (a.group * a.cache.kv_heads) + r.head] =
+            l == 0.f ? -kInf : (m + __builtin_log2f(l)) * kLn2;
+}
+
+__device__ inline float* part_stats(const AttentionArgs& a) {
+    const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
+    return a.part + rows * a.splits * a.cache.head_dim;
+}
+
+// ---- Few rows: tiles of 16 * NT rows, one tile, KV head and split of the
+// keys a workgroup.  Its 4 waves take 32-key blocks in turn, each wave with
+// its own running maximum and sums, joined through LDS at the end.  K comes
+// from global memory straight in the operand's layout (a lane has 16 bytes of
+// one key), V through a wave's own 32-key LDS buffer.
+constexpr uint32_t kFewThreads = 256, kFewWaves = 4, kBlockKeys = 32;
+
+template <uint32_t D>
+constexpr uint32_t kRowBytes = 2 * D + (D % 32 ? 0 : 32);   // LDS row of D 16-bit values: 8 dwords modulo 16, no bank conflicts
+
+template <uint32_t D, uint32_t NT>
+constexpr uint32_t few_lds_bytes() {
+    constexpr uint32_t stage = kFewWaves * kBlockKeys * kRowBytes<D>;
+    constexpr uint32_t join = kFewWaves * 16 * (D + 4) * 4;
+    return (stage > join ? stage : join) + kFewWaves * 16 * NT * 8;
+}
+
+template <uint32_t D, bool kE5M2, uint32_t NT>
+__global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
+    constexpr uint32_t M = 16 * NT, kFrags = (D + 31) / 32, kTiles = D / 16, kUnits = D / 8;
+    constexpr uint32_t kPer = kUnits / 2;            // 8-element units of V a lane stages for a block
+    constexpr uint32_t kUnitBytes = kE5M2 ? 8 : 16;
+    __shared__ __align__(16) uint8_t lds[few_lds_bytes<D, NT>()];
+    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
+    const uint64_t slot = blockIdx.x / a.cache.kv_heads;
+    if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
+        !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
+        flag(a.status);
+    const Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    if (!t.any) return;
+    const uint32_t splits = splits_of(t, a.split_len);
+    if (blockIdx.y && blockIdx.y >= splits) return;
+    const int32_t k0 = t.lo + static_cast<int32_t>(blockIdx.y * a.split_len);
+    const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.split_len) ? t.hi : k0 + static_cast<int32_t>(a.split_len);
+
+    const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16, c16 = lane % 16;
+
+    // Q^T operands: row c16 of each 16-row tile, elements 32 f + 8 g ..
+    u32x4 q[NT][kFrags];
+    float c[NT];
+    int32_t first[NT], last[NT];   // what the lane's row sees
+#pragma unroll
+    for (uint32_t nt = 0; nt < NT; ++nt) {
+        const uint32_t row = 16 * nt + c16;
+        const bool live = row < t.rows;
+        const RowAt r = row_at(t, t.row0 + (live ? row : 0), a.group, kv_head);
+        first[nt] = live ? a.mask.first(r.p) : 0;
+        last[nt] = live ? a.mask.last(r.p, t.seq.kv) : 0;
+        const SZ_GLOBAL uint16_t* from = gptr(a.q) + static_cast<uint64_t>(r.token) * a.q_stride + r.head * D;
+#pragma unroll
+        for (uint32_t f = 0; f < kFrags; ++f)
+            q[nt][f] = live && 32 * f + 8 * g < D ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 32 * f + 8 * g)
+                                                  : u32x4{0, 0, 0, 0};
+        c[nt] = a.scale * kLog2e;
+        if constexpr (kE5M2) {
+            float most = 0.f;
+#pragma unroll
+            for (uint32_t f = 0; f < kFrags; ++f) {
+                const f32x8 x = to_f32(q[nt][f]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
+            }
+            most = row_max(most);
+            const int32_t up = most > 0.f && most < kInf ? 14 - __builtin_amdgcn_frexp_expf(most) + 1 : 0;
+#pragma unroll
+            for (uint32_t f = 0; f < kFrags; ++f) {
+                f32x8 x = to_f32(q[nt][f]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_ldexpf(x[j], up);
+                q[nt][f] = pack<true>(x);
+            }
+            c[nt] = __builtin_amdgcn_ldexpf(c[nt], -up);
+        }
+        c[nt] = fmaxf(c[nt], 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
+    }
+
+    f32x4 o[NT][kTiles];
+    float m[NT], l[NT];
+#pragma unroll
+    for (uint32_t nt = 0; nt < NT; ++nt) {
+        m[nt] = -kInf;
+        l[nt] = 0.f;
+#pragma unroll
+        for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    uint8_t* stage = lds + wave * (kBlockKeys * kRowBytes<D>);
+    const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
+    const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
+    bool bad = false;
+
+    // page of the block's key `lane % 32`, or -1
+    auto pages_at = [&](int32_t kb) -> int32_t {
+        const int32_t p = kb + static_cast<int32_t>(lane % kBlockKeys);
+        if (p < t.seen || p >= k1) return -1;
+        const int32_t page = page_of(a.cache, a.batch, t.s, p);
+        bad |= page < 0;
+        return page;
+    };
+    u32x4 kreg[2][kFrags], vreg[kPer];
+    auto load_k = [&](int32_t kb, int32_t pages) {
+#pragma unroll
+        for (uint32_t kt = 0; kt < 2; ++kt) {
+            const int32_t page = __shfl(pages, kt * 16 + c16);
+            const SZ_GLOBAL uint8_t* from = pool_k;
+            if (page >= 0) from += slot_offset(a.cache, page, kb + static_cast<int32_t>(kt * 16 + c16));
+#pragma unroll
+            for (uint32_t f = 0; f < kFrags; ++f) {
+                u32x4 x = u32x4{0, 0, 0, 0};
+                if (page >= 0 && 32 * f + 8 * g < D) {
+                    if constexpr (kE5M2) {
+                        const u32x2 b = *reinterpret_cast<const SZ_GLOBAL u32x2*>(from + 32 * f + 8 * g);
+                        x[0] = b[0];
+                        x[1] = b[1];
+                    } else {
+                        x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 2 * (32 * f + 8 * g));
+                    }
+                }
+                kreg[kt][f] = x;
+            }
+        }
+    };
+    auto load_v = [&](int32_t kb, int32_t pages) {
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) {
+            const uint32_t u = lane + 64 * j, row = u / kUnits, col = u % kUnits;
+            const int32_t page = __shfl(pages, row);
+            u32x4 x = u32x4{0, 0, 0, 0};
+            if (page >= 0) {
+                const SZ_GLOBAL uint8_t* from =
+                    pool_v + slot_offset(a.cache, page, kb + static_cast<int32_t>(row)) + col * kUnitBytes;
+                if constexpr (kE5M2) {
+                    const u32x2 b = *reinterpret_cast<const SZ_GLOBAL u32x2*>(from);
+                    x[0] = b[0];
+                    x[1] = b[1];
+                } else {
+                    x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(from);
+                }
+            }
+            vreg[j] = x;
+        }
+    };
+
+    const int32_t step = kFewWaves * kBlockKeys;
+    int32_t kb = k0 + static_cast<int32_t>(wave * kBlockKeys);
+    int32_t pages = -1, next_pages = -1;
+    if (kb < k1) {
+        pages = pages_at(kb);
+        load_k(kb, pages);
+        load_v(kb, pages);
+        if (kb + step < k1) next_pages = pages_at(kb + step);
+    }
+    for (; kb < k1; kb += step) {
+        const bool more = kb + step < k1;
+        f32x4 s[NT][2];
+#pragma unroll
+        for (uint32_t kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t f = 0; f < kFrags; ++f) {
+                u32x4 x = kreg[kt][f];
+                if constexpr (kE5M2) x = expand(u32x2{x[0], x[1]});
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = mfma16<kE5M2>(x, q[nt][f], s[nt][kt]);
+            }
+        }
+        wave_lds_order();
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) {
+            const uint32_t u = lane + 64 * j, row = u / kUnits, col = u % kUnits;
+            u32x4 x = vreg[j];
+            if constexpr (kE5M2) x = expand(u32x2{x[0], x[1]});
+            *reinterpret_cast<u32x4*>(stage + row * kRowBytes<D> + col * 16) = x;
+        }
+        wave_lds_order();
+        const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
+        const int32_t this_pages_ok = static_cast<uint32_t>(here) == 0xFFFFFFFFu;
+        if (more) {
+            load_k(kb + step, next_pages);
+            load_v(kb + step, next_pages);
+            pages = next_pages;
+            next_pages = kb + 2 * step < k1 ? pages_at(kb + 2 * step) : -1;
+        }
+
+        // every row sees every key of the block?
+        const bool whole = this_pages_ok && kb >= a.mask.first(t.p1) &&
+                           kb + static_cast<int32_t>(kBlockKeys) <= a.mask.last(t.p0, t.seq.kv);
+        uint32_t seen[NT];   // bit 4 kt + j: the lane's row sees key 16 kt + 4 g + j
+        u32x4 p[NT];
+#pragma unroll
+        for (uint32_t nt = 0; nt < NT; ++nt) {
+            seen[nt] = 0xFF;
+            if (!whole) {
+                seen[nt] = 0;
+#pragma unroll
+                for (uint32_t kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        const uint32_t key = 16 * kt + 4 * g + j;
+                        const int32_t at = kb + static_cast<int32_t>(key);
+                        const bool sees = at >= first[nt] && at < last[nt] && (here >> key & 1);
+                        seen[nt] |= sees ? 1u << (4 * kt + j) : 0u;
+                        s[nt][kt][j] = sees ? s[nt][kt][j] : -kInf;
+                    }
+            }
+            float top = s[nt][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[nt][i / 4][i % 4]);
+            top = row_max(top) * c[nt];
+            const float was = m[nt], now = fmaxf(was, top);
+            const float base = now == -kInf ? 0.f : now;
+            if (__any(now > was)) {
+                const float r = __builtin_amdgcn_exp2f(was - base);
+                l[nt] *= r;
+#pragma unroll
+                for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] *= r;
+            }
+            m[nt] = now;
+            f32x8 e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][i / 4][i % 4], c[nt], -base));
+                l[nt] += e[i];
+            }
+            p[nt] = pack<kE5M2>(e);
+        }
+
+        const uint32_t r4 = c16 / 4, c4 = c16 % 4;
+        const uint8_t* read = stage + (4 * g + r4) * kRowBytes<D> + c4 * 8;
+#pragma unroll
+        for (uint32_t d = 0; d < kTiles; ++d) {
+            typedef __attribute__((address_space(3))) i16x4* lds4;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + d * 32));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kRowBytes<D> + d * 32));
+            const u32x2 lo2 = __builtin_bit_cast(u32x2, lo), hi2 = __builtin_bit_cast(u32x2, hi);
+            const u32x4 v = u32x4{lo2[0], lo2[1], hi2[0], hi2[1]};
+            const bool marked = !whole && __any(not_finite<kE5M2>(v));
+#pragma unroll
+            for (uint32_t nt = 0; nt < NT; ++nt) {
+                if (!marked) {
+                    o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
+                } else {
+                    f32x8 ones;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ones[i] = seen[nt] >> i & 1 ? 1.f : 0.f;
+                    o[nt][d] = add_marked<kE5M2>(Mfma16<kE5M2>{}, v, p[nt], pack<kE5M2>(ones), o[nt][d]);
+                }
+            }
+        }
+    }
+    if (__any(bad) && lane == 0) flag(a.status);
+
+    // ---- join the 4 waves
+    f32x2* stats = reinterpret_cast<f32x2*>(lds + few_lds_bytes<D, NT>() - kFewWaves * M * 8);   // [wave][row]
+#pragma unroll
+    for (uint32_t nt = 0; nt < NT; ++nt) {
+        const float sum = row_sum(l[nt]);
+        if (g == 0) stats[wave * M + 16 * nt + c16] = f32x2{m[nt], sum};
+    }
+    float* sums = reinterpret_cast<float*>(lds);   // [wave][16 rows][D + 4]
+#pragma unroll
+    for (uint32_t nt = 0; nt < NT; ++nt) {
+        __syncthreads();   // the stages, or the last tile's sums, have been read
+#pragma unroll
+        for (uint32_t d = 0; d < kTiles; ++d)
+            *reinterpret_cast<f32x4*>(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[nt][d];
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kFewThreads) {
+            const uint32_t row = i / (D / 4), d4 = i % (D / 4) * 4;
+            if (16 * nt + row >= t.rows) continue;
+            float top = -kInf;
+            f32x2 st[kFewWaves];
+#pragma unroll
+            for (uint32_t w = 0; w < kFewWaves; ++w) {
+                st[w] = stats[w * M + 16 * nt + row];
+                top = fmaxf(top, st[w][0]);
+            }
+            const float base = top == -kInf ? 0.f : top;
+            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            float sum = 0.f;
+#pragma unroll
+            for (uint32_t w = 0; w < kFewWaves; ++w) {
+                const float r = __builtin_amdgcn_exp2f(st[w][0] - base);
+                sum += r * st[w][1];
+                acc += r * *reinterpret_cast<const f32x4*>(sums + (w * 16 + row) * (D + 4) + d4);
+            }
+            const RowAt at = row_at(t, t.row0 + 16 * nt + row, a.group, kv_head);
+            if (splits <= 1) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                f32x4 y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] * inv;
+                *reinterpret_cast<SZ_GLOBAL u32x2*>(gptr(a.out) + static_cast<uint64_t>(at.token) * a.out_stride +
+                                                    at.head * D + d4) =
+                    __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
+                if (d4 == 0) put_lse(a, at, base, sum);
+            } else {
+                const uint64_t r = (static_cast<uint64_t>(at.token) * (a.group * a.cache.kv_heads) + at.head) * a.splits +
+                                   blockIdx.y;
+                *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
+                if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
+            }
+        }
+    }
+}
+
+// Joins the splits of each row: one wave a row, D / 64 (or fewer lanes) sums a lane.
+template <uint32_t D>
+__global__ __launch_bounds__(256) void k_join(AttentionArgs a) {
+    const uint32_t heads = a.group * a.cache.kv_heads;
+    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
+    const uint32_t lane = threadIdx.x % 64;
+    if (row >= static_cast<uint64_t>(a.batch.total_tokens) * heads) return;
+    const uint32_t token = uniform(static_cast<uint32_t>(row / heads)), head = static_cast<uint32_t>(row % heads);
+    const uint32_t s = seq_of_token(a.batch, token);
+    if (s >= a.batch.num_seqs) return;
+    Tile t{};
+    t.seq = span_of(a.batch, s);
+    if (!t.seq.ok || static_cast<int32_t>(token) < t.seq.begin) return;
+    // the tile that had the row
+    const uint32_t at = (token - t.seq.begin) * a.group + head % a.group;
+    t.row0 = at / a.tile * a.tile;
+    const uint32_t rows = static_cast<uint32_t>(t.seq.n) * a.group - t.row0;
+    t.rows = rows < a.tile ? rows : a.tile;
+    tile_range(t, a.mask, a.group);
+    const uint32_t splits = splits_of(t, a.split_len);
+    if (splits <= 1) return;   // written by its workgroup
+    const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a))) + row * a.splits;
+    float top = -kInf;
+    for (uint32_t z = 0; z < splits; ++z)
+        if (stats[z][1] != 0.f) top = fmaxf(top, stats[z][0]);
+    const float base = top == -kInf ? 0.f : top;
+    const SZ_GLOBAL float* part = gptr(a.part) + row * a.splits * D;
+    constexpr uint32_t kPer = (D + 63) / 64;
+    float acc[kPer] = {};
+    float sum = 0.f;
+    for (uint32_t z = 0; z < splits; ++z) {
+        const f32x2 st = stats[z];
+        if (st[1] == 0.f) continue;
+        const float r = __builtin_amdgcn_exp2f(st[0] - base);
+        sum += r * st[1];
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; ++i) {
+            const uint32_t d = lane + 64 * i;
+            if (d < D) acc[i] += r * part[z * D + d];
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+        const uint32_t d = lane + 64 * i;
+        if (d >= D) continue;
+        const __bf16 y = static_cast<__bf16>(sum == 0.f ? 0.f : acc[i] / sum);
+        gptr(a.out)[static_cast<uint64_t>(token) * a.out_stride + head * D + d] = __builtin_bit_cast(uint16_t, y);
+    }
+    if (lane == 0) put_lse(a, RowAt{token, head, 0}, base, sum);
+}
+
+template <uint32_t D, bool kE5M2>
+hipError_t attend(const AttentionArgs& a, hipStream_t s) {
+    const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
+    const dim3 grid(static_cast<uint32_t>(slots * a.cache.kv_heads), a.splits);
+    if (a.tile == 16) k_attend_few<D, kE5M2, 1><<<grid, kFewThreads, 0, s>>>(a);
+    else k_attend_few<D, kE5M2, 2><<<grid, kFewThreads, 0, s>>>(a);
+    if (a.splits > 1) {
+        const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
+        k_join<D><<<static_cast<uint32_t>((rows + 3) / 4), 256, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
+    switch (a.cache.head_dim) {
+        case 64: return a.e5m2 ? attend<64, true>(a, s) : attend<64, false>(a, s);
+        case 80: return a.e5m2 ? attend<80, true>(a, s) : attend<80, false>(a, s);
+        case 96: return a.e5m2 ? attend<96, true>(a, s) : attend<96, false>(a, s);
+        case 128: return a.e5m2 ? attend<128, true>(a, s) : attend<128, false>(a, s);
+        default: return a.e5m2 ? attend<256, true>(a, s) : attend<256, false>(a, s);
+    }
+}
+
+}  // namespace kvi

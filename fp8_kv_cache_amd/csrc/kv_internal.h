@@ -1,0 +1,198 @@
+// kv_internal.h -- the index arithmetic of the paged KV cache (shared by its
+// kernels and its host checks) and the launch interfaces; the calls are
+// documented in include/paged_kv.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sz_internal.h"
+
+namespace kvi {
+
+#define KV_HD __host__ __device__ inline
+
+struct Cache {
+    uint8_t* k;
+    uint8_t* v;
+    uint64_t page_stride, token_stride, head_stride;   // bytes
+    uint32_t num_pages, log2_page, kv_heads, head_dim;
+};
+
+struct Batch {
+    const int32_t* pages;
+    const int32_t* cu;
+    const int32_t* kv_lens;
+    uint64_t pages_stride;
+    uint32_t pages_per_seq, num_seqs, total_tokens, max_tokens, max_kv_len;
+};
+
+// One sequence of the batch as the device data give it.
+struct Span {
+    int32_t begin, n, kv;
+    bool ok;
+    KV_HD int32_t first() const { return kv - n; }   // position of its first new token (may be negative)
+};
+
+KV_HD Span span_of(const Batch& b, uint32_t s) {
+    Span p;
+    const int32_t lo = b.cu[s], hi = b.cu[s + 1];
+    p.begin = lo;
+    p.kv = b.kv_lens[s];
+    p.ok = lo >= 0 && hi >= lo && static_cast<uint32_t>(hi) <= b.total_tokens &&
+           static_cast<uint32_t>(hi - lo) <= b.max_tokens && p.kv >= 0 &&
+           static_cast<uint32_t>(p.kv) <= b.max_kv_len;
+    p.n = p.ok ? hi - lo : 0;
+    return p;
+}
+
+// The sequence that has token row t: cu[s] <= t < cu[s + 1], or num_seqs
+// where none has (padding behind the last).  Terminates, and answers inside
+// [0, num_seqs], whatever cu holds; callers compare t with the span found.
+KV_HD uint32_t seq_of_token(const Batch& b, uint32_t t) {
+    uint32_t lo = 0, hi = b.num_seqs;   // the first s with cu[s + 1] > t
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (b.cu[mid + 1] > static_cast<int32_t>(t)) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Page of a sequence's position p >= 0, or -1: past the table, or not a
+// page of the pool.
+KV_HD int32_t page_of(const Cache& c, const Batch& b, uint32_t s, int32_t p) {
+    const uint32_t i = static_cast<uint32_t>(p) >> c.log2_page;
+    if (i >= b.pages_per_seq) return -1;
+    const int32_t page = b.pages[s * b.pages_stride + i];
+    return static_cast<uint32_t>(page) < c.num_pages ? page : -1;
+}
+
+// Byte offset in a pool of slot p % page_size of `page` (not negative), head 0.
+KV_HD uint64_t slot_offset(const Cache& c, int32_t page, int32_t p) {
+    return static_cast<uint64_t>(page) * c.page_stride +
+           static_cast<uint64_t>(static_cast<uint32_t>(p) & ((1u << c.log2_page) - 1)) * c.token_stride;
+}
+
+// ---- Attention's work: the rows of a sequence under one KV head are its
+// (token, query head of the group) pairs, token-major, n * group of them,
+// cut into tiles of M.  Sequence s has the tile slots from
+// floor(cu[s] * group / M) + s: floor((a + x) / M) - floor(a / M) + 1 >=
+// ceil(x / M), so its tiles fit before the next sequence's, and a workgroup
+// finds its tile by a search in cu, with no table to build first.
+KV_HD uint64_t tile_slot(const Batch& b, uint32_t s, uint32_t group, uint32_t M) {
+    const int32_t c = b.cu[s];
+    return static_cast<uint64_t>(c < 0 ? 0 : c) * group / M + s;
+}
+KV_HD uint64_t tile_slots(const Batch& b, uint32_t group, uint32_t M) {
+    return static_cast<uint64_t>(b.total_tokens) * group / M + b.num_seqs;
+}
+
+struct Tile {
+    Span seq;
+    uint32_t s;
+    uint32_t row0, rows;      // first row of the tile in the sequence, and how many
+    int32_t seen, lo, hi;     // positions that any of its rows sees: [seen, hi); lo is seen, down to a multiple of 32
+    int32_t p0, p1;           // positions of its first and last token
+    bool any;
+};
+
+struct Mask {
+    uint32_t causal, window;
+    // row at position p of a sequence of kv tokens sees [first(p), last(p))
+    KV_HD int32_t first(int32_t p) const {
+        return window && p >= 0 && static_cast<uint32_t>(p) >= window ? p + 1 - static_cast<int32_t>(window) : 0;
+    }
+    KV_HD int32_t last(int32_t p, int32_t kv) const { return causal ? (p < 0 ? 0 : p + 1) : (p < 0 ? 0 : kv); }
+};
+
+KV_HD void tile_range(Tile& t, const Mask& mask, uint32_t group) {
+    t.p0 = t.seq.first() + static_cast<int32_t>(t.row0 / group);
+    t.p1 = t.seq.first() + static_cast<int32_t>((t.row0 + t.rows - 1) / group);
+    t.seen = mask.first(t.p0);
+    t.lo = t.seen & ~31;
+    t.hi = mask.last(t.p1, t.seq.kv);
+}
+
+// The tile in `slot`; any = false where the slot has none.
+KV_HD Tile tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t group, uint32_t M) {
+    Tile t{};
+    uint32_t lo = 0, hi = b.num_seqs;   // the last s with tile_slot(s) <= slot
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (tile_slot(b, mid, group, M) <= slot) lo = mid;
+        else hi = mid;
+    }
+    t.s = lo;
+    t.seq = span_of(b, lo);
+    const uint64_t first = tile_slot(b, lo, group, M);
+    if (slot < first || !t.seq.ok) return t;
+    const uint64_t row0 = (slot - first) * M, rows = static_cast<uint64_t>(t.seq.n) * group;
+    if (row0 >= rows) return t;
+    t.any = true;
+    t.row0 = static_cast<uint32_t>(row0);
+    t.rows = static_cast<uint32_t>(rows - row0 < M ? rows - row0 : M);
+    tile_range(t, mask, group);
+    return t;
+}
+
+// Splits of a tile's positions: split z has [lo + z * len, lo + (z + 1) * len) of [lo, hi).
+KV_HD uint32_t splits_of(const Tile& t, uint32_t len) {
+    return t.hi > t.lo ? (static_cast<uint32_t>(t.hi - t.lo) + len - 1) / len : 0;
+}
+
+// ---- launch interfaces
+
+struct AppendArgs {
+    Cache cache;
+    Batch batch;
+    const uint16_t *k, *v, *q;
+    uint16_t* q_out;
+    uint64_t k_stride, v_stride, q_stride, q_out_stride;   // elements
+    const float* cos_sin;
+    const uint16_t *q_norm, *k_norm;
+    float eps;
+    uint32_t q_heads, rotary_dim, max_positions, interleaved;
+    int32_t* status;
+    bool e5m2;
+};
+
+struct CopyArgs {
+    Cache cache;
+    Batch batch;
+    uint8_t *k, *v;                // the layer tensors
+    uint64_t k_stride, v_stride;   // bytes
+    uint32_t head_bytes;
+    int32_t* status;
+};
+
+struct AttentionArgs {
+    Cache cache;
+    Batch batch;
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    uint64_t q_stride, out_stride;   // elements
+    float scale;
+    Mask mask;
+    uint32_t group;                  // query heads of a KV head
+    uint32_t tile;                   // rows of a tile (attention_plan)
+    uint32_t splits, split_len;      // at most `splits` of split_len positions each
+    float* part;                     // workspace: [row][split][head_dim] sums, then [row][split] (max, sum)
+    int32_t* status;
+    bool e5m2;
+};
+
+struct AttentionPlan {
+    uint32_t tile, splits, split_len;
+    uint64_t workspace_bytes;
+};
+AttentionPlan attention_plan(uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint32_t num_seqs, uint32_t total_tokens,
+                             uint32_t max_tokens, uint32_t max_kv_len, uint32_t window);
+
+hipError_t launch_append(const AppendArgs& a, hipStream_t s);
+hipError_t launch_gather(const CopyArgs& a, hipStream_t s);
+hipError_t launch_scatter(const CopyArgs& a, hipStream_t s);
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
+
+}  // namespace kvi

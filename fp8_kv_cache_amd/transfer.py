@@ -23,11 +23,15 @@ once, as two machines' NICs would).
 
 Both return the received tensors, so callers can check bit-exactness.
 Streams run at the default priority.
+
+PagedLink ships between paged caches: the sender's layers are gathered out
+of their pages, shipped, and scattered into the receiver's pages.
 """
 import torch
 
 from . import SZ_DTYPE_BF16, check, pointer_table, sz_compress_batched, sz_compress_workspace_bytes_batched, \
     sz_decode, sz_max_compressed_bytes
+from . import paged
 from .codec import ELEMENT_BYTES
 
 
@@ -157,3 +161,33 @@ class Link:
 
     def compress_statuses(self):
         return self.fused_status.cpu().tolist()
+
+
+class PagedLink:
+    """Ships the cached tokens of a batch of sequences, all layers, from one
+    machine's paged caches into another's: `layers` caches of the given head
+    shape and dtype, `tokens` token rows in all."""
+
+    def __init__(self, layers, tokens, kv_heads, head_dim, dtype=SZ_DTYPE_BF16, device="cuda", group=8):
+        self.shape = (tokens, kv_heads, head_dim)
+        torch_dtype = torch.bfloat16 if dtype == SZ_DTYPE_BF16 else torch.float8_e5m2
+        self.torch_dtype, self.layers = torch_dtype, layers
+        self.link = Link(2 * layers, tokens * kv_heads * head_dim, dtype, device, group)
+        self.rows = [torch.empty(self.shape, dtype=torch_dtype, device=device) for _ in range(2 * layers)]
+
+    def ship(self, caches, batch, to_caches, to_batch, compressed=True):
+        """The batch's rows of caches[l] into to_batch's pages of
+        to_caches[l], for every layer l.  The batches have the same tokens
+        (cu_tokens of the whole sequences, kv_lens their lengths), each with
+        its own machine's page table.  Rows behind the last sequence travel
+        as they are and are not written."""
+        for sent, side in ((caches, batch), (to_caches, to_batch)):
+            if len(sent) != self.layers or side.total_tokens != self.shape[0]:
+                raise ValueError(f"this link ships {self.layers} layers of {self.shape[0]} token rows")
+        for l, cache in enumerate(caches):
+            paged.gather(cache, batch, self.rows[2 * l], self.rows[2 * l + 1])
+        ship = self.link.ship_compressed if compressed else self.link.ship_raw
+        landed = [x.view(self.torch_dtype).view(self.shape)
+                  for x in ship([x.view(torch.uint8).reshape(-1) for x in self.rows])]
+        for l, cache in enumerate(to_caches):
+            paged.scatter(cache, to_batch, landed[2 * l], landed[2 * l + 1])

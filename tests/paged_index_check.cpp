@@ -1,0 +1,148 @@
+// Host check of the paged cache's index arithmetic (kv_internal.h, the
+// functions its kernels call), over random and hostile batches:
+// - every token of every well-formed sequence is found by seq_of_token, and
+//   every (token, query head) row lies in exactly one tile, for each tile
+//   size, at a slot below tile_slots();
+// - a tile's rows, positions and key range are its sequence's, its splits
+//   cover its keys once, and the range holds what every row's mask sees;
+// - with token ranges and lengths that are anything at all, every read of
+//   cu stays in its array (checked by guard values through a copy on the
+//   heap of exactly that size, run under AddressSanitizer), and every tile
+//   that claims rows claims rows inside [0, total_tokens);
+// - page_of gives -1 for every id outside the pool and index past the table.
+// Prints "ok <checks>".
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+
+#include "kv_internal.h"
+
+using namespace kvi;
+
+static long checks = 0;
+#define CHECK(x)                                                  \
+    do {                                                          \
+        ++checks;                                                 \
+        if (!(x)) {                                               \
+            std::printf("failed at %d: %s\n", __LINE__, #x);      \
+            std::exit(1);                                         \
+        }                                                         \
+    } while (0)
+
+struct Data {
+    std::vector<int32_t> cu, kv, pages;
+    Batch b{};
+    void bind(uint32_t total, uint32_t most, uint32_t most_kv, uint32_t per_seq) {
+        b.cu = cu.data();
+        b.kv_lens = kv.data();
+        b.pages = pages.data();
+        b.num_seqs = static_cast<uint32_t>(kv.size());
+        b.total_tokens = total;
+        b.max_tokens = most;
+        b.max_kv_len = most_kv;
+        b.pages_per_seq = per_seq;
+        b.pages_stride = per_seq;
+    }
+};
+
+int main() {
+    std::mt19937 rng(1);
+    auto upto = [&](int n) { return static_cast<int>(rng() % static_cast<unsigned>(n + 1)); };
+    for (int round = 0; round < 400; ++round) {
+        Data d;
+        const int seqs = 1 + upto(9);
+        std::vector<int> n(seqs);
+        int at = upto(1) * upto(3);
+        d.cu.push_back(at);
+        int most = 1, most_kv = 0;
+        for (int s = 0; s < seqs; ++s) {
+            n[s] = upto(2) ? upto(40) : upto(300);
+            if (!upto(3)) n[s] = 0;
+            at += n[s];
+            d.cu.push_back(at);
+            d.kv.push_back(upto(4) ? n[s] + upto(500) : upto(n[s]));
+            most = n[s] > most ? n[s] : most;
+            most_kv = d.kv[s] > most_kv ? d.kv[s] : most_kv;
+        }
+        d.bind(at + upto(5), most, most_kv, 1);
+        for (uint32_t t = 0; t < d.b.total_tokens; ++t) {
+            const uint32_t s = seq_of_token(d.b, t);
+            CHECK(s <= d.b.num_seqs);
+            if (static_cast<int>(t) >= at) CHECK(s == d.b.num_seqs);
+            else if (static_cast<int>(t) >= d.cu[0]) CHECK(d.cu[s] <= static_cast<int>(t) && static_cast<int>(t) < d.cu[s + 1]);
+        }
+        for (uint32_t group : {1u, 3u, 4u, 8u, 64u})
+            for (uint32_t M : {16u, 32u, 64u, 128u, 256u}) {
+                const Mask mask{upto(3) ? 1u : 0u, 0};
+                Mask m = mask;
+                if (m.causal && upto(1)) m.window = 1 + upto(200);
+                std::vector<std::vector<int>> had(seqs);
+                for (int s = 0; s < seqs; ++s) had[s].assign(n[s] * group, 0);
+                for (uint64_t slot = 0; slot < tile_slots(d.b, group, M); ++slot) {
+                    const Tile t = tile_of(d.b, m, slot, group, M);
+                    if (!t.any) continue;
+                    CHECK(t.rows >= 1 && t.rows <= M && t.row0 % M == 0);
+                    for (uint32_t r = 0; r < t.rows; ++r) {
+                        ++had[t.s][t.row0 + r];
+                        const int32_t p = t.seq.first() + static_cast<int32_t>((t.row0 + r) / group);
+                        const int32_t lo = m.first(p), hi = m.last(p, t.seq.kv);
+                        CHECK(p >= t.p0 && p <= t.p1);
+                        if (hi > lo) CHECK(lo >= t.seen && hi <= t.hi);
+                        CHECK(hi <= t.seq.kv);
+                    }
+                    CHECK(t.lo % 32 == 0 && t.lo <= t.seen && t.lo > t.seen - 32 && t.lo >= 0);
+                    const uint32_t len = 128u << upto(3), splits = splits_of(t, len);
+                    if (t.hi > t.lo)
+                        CHECK(t.lo + static_cast<int64_t>(splits) * len >= t.hi && t.lo + static_cast<int64_t>(splits - 1) * len < t.hi);
+                    else CHECK(splits == 0);
+                }
+                for (auto& rows : had)
+                    for (int times : rows) CHECK(times == 1);
+            }
+    }
+    // anything at all in cu and kv_lens
+    for (int round = 0; round < 2000; ++round) {
+        Data d;
+        const int seqs = 1 + upto(6);
+        auto wild = [&]() -> int32_t {
+            switch (upto(4)) {
+                case 0: return static_cast<int32_t>(rng());
+                case 1: return 2147483647 - upto(2);
+                case 2: return -upto(2000);
+                default: return upto(60);
+            }
+        };
+        for (int s = 0; s <= seqs; ++s) d.cu.push_back(wild());
+        for (int s = 0; s < seqs; ++s) d.kv.push_back(wild());
+        d.cu.shrink_to_fit();
+        d.bind(1 + upto(60), 1 + upto(60), upto(100), 1);
+        for (uint32_t t = 0; t < d.b.total_tokens; ++t) CHECK(seq_of_token(d.b, t) <= d.b.num_seqs);
+        for (uint32_t group : {1u, 8u})
+            for (uint64_t slot = 0; slot < tile_slots(d.b, group, 16); ++slot) {
+                const Tile t = tile_of(d.b, Mask{1, 0}, slot, group, 16);
+                if (!t.any) continue;
+                const int64_t last = t.seq.begin + static_cast<int64_t>(t.row0 + t.rows - 1) / group;
+                CHECK(t.seq.begin >= 0 && last < static_cast<int64_t>(d.b.total_tokens));
+                CHECK(t.hi <= static_cast<int32_t>(d.b.max_kv_len) && t.lo >= 0);
+            }
+    }
+    // pages
+    Cache c{};
+    c.num_pages = 7;
+    c.log2_page = 4;
+    c.page_stride = uint64_t(1) << 33;
+    c.token_stride = 512;
+    Data d;
+    d.cu = {0, 1, 2};
+    d.kv = {1, 1};
+    d.pages = {0, 6, 7, -1, 2147483647, -2147483647 - 1, 3, 5};
+    d.bind(2, 1, 100, 4);
+    const int32_t want[8] = {0, 6, -1, -1, -1, -1, 3, 5};
+    for (uint32_t s = 0; s < 2; ++s)
+        for (int32_t p = 0; p < 200; ++p) CHECK(page_of(c, d.b, s, p) == (p / 16 < 4 ? want[4 * s + p / 16] : -1));
+    CHECK(page_of(c, d.b, 1, 2147483647) == -1);
+    CHECK(slot_offset(c, 6, 16 * 5 + 3) == 6 * c.page_stride + 3 * 512);
+    std::printf("ok %ld\n", checks);
+    return 0;
+}
