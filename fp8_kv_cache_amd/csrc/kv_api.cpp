@@ -233,7 +233,7 @@ kvi::AttentionPlan kvi::attention_plan(uint32_t kv_heads, uint32_t group, uint32
                                        uint32_t window) {
     AttentionPlan p{};
     const uint64_t most_rows = static_cast<uint64_t>(max_tokens) * group;
-    p.tile = most_rows <= 16 ? 16 : 32;
+    p.tile = most_rows <= 16 ? 16 : most_rows <= 64 ? 32 : 128;
     // positions that a tile can see, and tiles that the call can have
     uint64_t range = max_kv_len;
     if (window && static_cast<uint64_t>(window) + p.tile + 32 < range) range = static_cast<uint64_t>(window) + p.tile + 32;

@@ -71,6 +71,16 @@ __device__ inline u32x4 pack(f32x8 x) {   // to the matrix cores' 16-bit type, n
     else return __builtin_bit_cast(u32x4, __builtin_convertvector(x, bf16x8));
 }
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <bool kE5M2>
+__device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (kE5M2)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
 // max or sum over the lanes that hold the same query row (lane, lane ^ 16, lane ^ 32, lane ^ 48)
 __device__ inline float swap16(float x, bool hi) {
     const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -100,49 +110,32 @@ __device__ inline bool not_finite(u32x4 x) {
     return any;
 }
 
-// Splits 8 packed values into the finite ones (others 0) and markers (1.0)
-// of those that bring +Inf (+Inf, NaN) and -Inf (-Inf, NaN) into a sum.
+// 8 packed values with 0 for the Inf and NaN among them.
 template <bool kE5M2>
-__device__ inline void part_values(u32x4& x, u32x4& up, u32x4& down) {
-    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u, kOne = kE5M2 ? 0x3C00u : 0x3F80u;
-    up = down = u32x4{0, 0, 0, 0};
+__device__ inline u32x4 finite_part(u32x4 x) {
+    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-            const uint32_t v = (x[i] >> h) & 0xFFFFu;
-            if ((v & kExp) != kExp) continue;
-            const bool nan = (v & (0x7FFFu & ~kExp)) != 0, minus = v >> 15;
-            if (nan || !minus) up[i] |= kOne << h;
-            if (nan || minus) down[i] |= kOne << h;
-            x[i] &= ~(0xFFFFu << h);
-        }
-}
-
-// Accumulates V^T P^T where the rows of a tile see different keys and V
-// holds Inf or NaN: a weight of 0 would not keep them out of the product.
-// Their markers meet the mask instead of the weights, and a row that sees
-// one gets it added.
-template <bool kE5M2, typename F, typename Acc>
-__device__ inline Acc add_marked(F mfma, u32x4 v, u32x4 p, u32x4 seen, Acc o) {
-    u32x4 up, down;
-    part_values<kE5M2>(v, up, down);
-    o = mfma(v, p, o);
-    Acc a{}, b{};
-    a = mfma(up, seen, a);
-    b = mfma(down, seen, b);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Acc) / 4); ++i) {
-        if (a[i] > 0.f) o[i] += kInf;
-        if (b[i] > 0.f) o[i] -= kInf;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (x[i] & kExp) == kExp ? 0u : x[i] & 0xFFFFu;
+        const uint32_t hi = (x[i] & (kExp << 16)) == (kExp << 16) ? 0u : x[i] & 0xFFFF0000u;
+        x[i] = lo | hi;
     }
-    return o;
+    return x;
 }
 
+// Adds the Inf and NaN among 4 packed values to 4 sums.
 template <bool kE5M2>
-struct Mfma16 {
-    __device__ f32x4 operator()(u32x4 a, u32x4 b, f32x4 c) const { return mfma16<kE5M2>(a, b, c); }
-};
+__device__ inline void add_not_finite(u32x2 x, float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t v = x[i / 2] >> (i % 2 * 16) & 0xFFFFu;
+        if constexpr (kE5M2) {
+            if ((v & 0x7C00u) == 0x7C00u) o[i] += static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(v)));
+        } else {
+            if ((v & 0x7F80u) == 0x7F80u) o[i] += __uint_as_float(v << 16);
+        }
+    }
+}
 
 // LDS order inside one wave: its LDS instructions execute in order; this
 // keeps the compiler from moving one lane's reads over another's writes.
@@ -364,13 +357,10 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
         // every row sees every key of the block?
         const bool whole = this_pages_ok && kb >= a.mask.first(t.p1) &&
                            kb + static_cast<int32_t>(kBlockKeys) <= a.mask.last(t.p0, t.seq.kv);
-        uint32_t seen[NT];   // bit 4 kt + j: the lane's row sees key 16 kt + 4 g + j
         u32x4 p[NT];
 #pragma unroll
         for (uint32_t nt = 0; nt < NT; ++nt) {
-            seen[nt] = 0xFF;
             if (!whole) {
-                seen[nt] = 0;
 #pragma unroll
                 for (uint32_t kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -378,7 +368,6 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
                         const uint32_t key = 16 * kt + 4 * g + j;
                         const int32_t at = kb + static_cast<int32_t>(key);
                         const bool sees = at >= first[nt] && at < last[nt] && (here >> key & 1);
-                        seen[nt] |= sees ? 1u << (4 * kt + j) : 0u;
                         s[nt][kt][j] = sees ? s[nt][kt][j] : -kInf;
                     }
             }
@@ -404,25 +393,45 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
             p[nt] = pack<kE5M2>(e);
         }
 
-        const uint32_t r4 = c16 / 4, c4 = c16 % 4;
-        const uint8_t* read = stage + (4 * g + r4) * kRowBytes<D> + c4 * 8;
-#pragma unroll
-        for (uint32_t d = 0; d < kTiles; ++d) {
+        const uint8_t* read = stage + (4 * g + c16 / 4) * kRowBytes<D> + c16 % 4 * 8;
+        auto value = [&](uint32_t d) {   // V^T operand of elements 16 d ..
             typedef __attribute__((address_space(3))) i16x4* lds4;
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + d * 32));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kRowBytes<D> + d * 32));
-            const u32x2 lo2 = __builtin_bit_cast(u32x2, lo), hi2 = __builtin_bit_cast(u32x2, hi);
-            const u32x4 v = u32x4{lo2[0], lo2[1], hi2[0], hi2[1]};
-            const bool marked = !whole && __any(not_finite<kE5M2>(v));
+            const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + d * 32)));
+            const u32x2 hi = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kRowBytes<D> + d * 32)));
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        };
+        bool special = false;
+        if (!whole)
 #pragma unroll
-            for (uint32_t nt = 0; nt < NT; ++nt) {
-                if (!marked) {
-                    o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
-                } else {
-                    f32x8 ones;
+            for (uint32_t d = 0; d < kTiles; ++d) special |= not_finite<kE5M2>(value(d));
+        if (!__any(special)) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ones[i] = seen[nt] >> i & 1 ? 1.f : 0.f;
-                    o[nt][d] = add_marked<kE5M2>(Mfma16<kE5M2>{}, v, p[nt], pack<kE5M2>(ones), o[nt][d]);
+            for (uint32_t d = 0; d < kTiles; ++d) {
+                const u32x4 v = value(d);
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; ++nt) o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
+            }
+        } else {
+            // a weight of 0 would not keep an Inf or NaN that a row does not see out of the product
+#pragma unroll
+            for (uint32_t d = 0; d < kTiles; ++d) {
+                const u32x4 v = finite_part<kE5M2>(value(d));
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; ++nt) o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
+            }
+#pragma unroll 1
+            for (uint32_t key = 0; key < kBlockKeys; ++key) {
+                const int32_t at = kb + static_cast<int32_t>(key);
+#pragma unroll
+                for (uint32_t nt = 0; nt < NT; ++nt) {
+                    if (at < first[nt] || at >= last[nt] || !(here >> key & 1)) continue;
+#pragma unroll
+                    for (uint32_t d = 0; d < kTiles; ++d) {
+                        float x[4] = {o[nt][d][0], o[nt][d][1], o[nt][d][2], o[nt][d][3]};
+                        add_not_finite<kE5M2>(*reinterpret_cast<const u32x2*>(stage + key * kRowBytes<D> + 32 * d + 8 * g), x);
+                        o[nt][d] = f32x4{x[0], x[1], x[2], x[3]};
+                    }
                 }
             }
         }
@@ -484,6 +493,285 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
     }
 }
 
+// ---- Many rows: tiles of 128 rows, 32 a wave; the 4 waves share K and V
+// tiles of N keys in LDS, two of each, so that one barrier a tile does: the
+// next tile's 16-byte pieces are on their way into registers while this one
+// is multiplied, and are put into the other buffer behind it.
+constexpr uint32_t kTileThreads = 256, kTileRows = 128;
+
+template <uint32_t D>
+constexpr uint32_t kKeyRow = 2 * D + 16;                          // K rows in LDS: 16-byte reads of 16 rows meet all banks
+template <uint32_t D>
+constexpr uint32_t kValueRow = ((2 * D + 63) / 64 | 1) * 64;      // V rows: 4 rows of 64 bytes meet all banks
+
+template <uint32_t D, bool kE5M2, uint32_t N>
+__global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(AttentionArgs a) {
+    constexpr uint32_t M = kTileRows, kFrags = D / 16, kTiles = (D + 31) / 32, kUnits = D / 8, kSub = N / 32;
+    constexpr uint32_t kPieces = N * kUnits, kPer = (kPieces + kTileThreads - 1) / kTileThreads;
+    constexpr uint32_t kBuffer = N * (kKeyRow<D> + kValueRow<D>);
+    __shared__ __align__(16) uint8_t lds[2 * kBuffer];
+    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
+    const uint64_t slot = blockIdx.x / a.cache.kv_heads;
+    if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
+        !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
+        flag(a.status);
+    const Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    if (!t.any) return;
+    const uint32_t splits = splits_of(t, a.split_len);
+    if (blockIdx.y && blockIdx.y >= splits) return;
+    const int32_t k0 = t.lo + static_cast<int32_t>(blockIdx.y * a.split_len);
+    const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.split_len) ? t.hi : k0 + static_cast<int32_t>(a.split_len);
+
+    const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), half = lane / 32, c32 = lane % 32;
+
+    // Q^T operands: the lane's row, elements 16 f + 8 half ..
+    const uint32_t row = 32 * wave + c32;
+    const bool live = row < t.rows;
+    const RowAt at = row_at(t, t.row0 + (live ? row : 0), a.group, kv_head);
+    const int32_t first = live ? a.mask.first(at.p) : 0, last = live ? a.mask.last(at.p, t.seq.kv) : 0;
+    // positions of the wave's first and last row: what all of its rows see, and what any does
+    const bool wave_live = 32 * wave < t.rows;
+    const uint32_t wave_end = 32 * wave + 31 < t.rows ? 32 * wave + 31 : t.rows - 1;
+    const int32_t wave_p0 = t.seq.first() + static_cast<int32_t>((t.row0 + (wave_live ? 32 * wave : 0)) / a.group);
+    const int32_t wave_p1 = t.seq.first() + static_cast<int32_t>((t.row0 + wave_end) / a.group);
+    const int32_t all_from = a.mask.first(wave_p1), all_to = a.mask.last(wave_p0, t.seq.kv);
+    const int32_t any_from = a.mask.first(wave_p0), any_to = wave_live ? a.mask.last(wave_p1, t.seq.kv) : 0;
+
+    u32x4 q[kFrags];
+    const SZ_GLOBAL uint16_t* from = gptr(a.q) + static_cast<uint64_t>(at.token) * a.q_stride + at.head * D;
+#pragma unroll
+    for (uint32_t f = 0; f < kFrags; ++f)
+        q[f] = live ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 16 * f + 8 * half) : u32x4{0, 0, 0, 0};
+    float c = a.scale * kLog2e;
+    if constexpr (kE5M2) {
+        float most = 0.f;
+#pragma unroll
+        for (uint32_t f = 0; f < kFrags; ++f) {
+            const f32x8 x = to_f32(q[f]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
+        }
+        most = fmaxf(swap32(most, false), swap32(most, true));
+        const int32_t up = most > 0.f && most < kInf ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+#pragma unroll
+        for (uint32_t f = 0; f < kFrags; ++f) {
+            f32x8 x = to_f32(q[f]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_ldexpf(x[j], up);
+            q[f] = pack<true>(x);
+        }
+        c = __builtin_amdgcn_ldexpf(c, -up);
+    }
+    c = fmaxf(c, 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
+
+    f32x16 o[kTiles];
+#pragma unroll
+    for (uint32_t d = 0; d < kTiles; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float m = -kInf, l = 0.f;
+
+    const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
+    const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
+    bool bad = false;
+    auto pages_at = [&](int32_t kb) -> int32_t {   // page of the tile's key `lane % N`, or -1
+        const int32_t p = kb + static_cast<int32_t>(lane % N);
+        if (p < t.seen || p >= k1) return -1;
+        const int32_t page = page_of(a.cache, a.batch, t.s, p);
+        bad |= page < 0;
+        return page;
+    };
+    u32x4 kreg[kPer], vreg[kPer];
+    auto load = [&](int32_t kb, int32_t pages) {
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) {
+            const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits, col = u % kUnits;
+            const int32_t page = __shfl(pages, key % 64);
+            u32x4 x = u32x4{0, 0, 0, 0}, y = x;
+            if (page >= 0 && u < kPieces) {
+                const uint64_t off = slot_offset(a.cache, page, kb + static_cast<int32_t>(key)) + col * (kE5M2 ? 8 : 16);
+                if constexpr (kE5M2) {
+                    const u32x2 xb = *reinterpret_cast<const SZ_GLOBAL u32x2*>(pool_k + off);
+                    const u32x2 yb = *reinterpret_cast<const SZ_GLOBAL u32x2*>(pool_v + off);
+                    x = u32x4{xb[0], xb[1], 0, 0};
+                    y = u32x4{yb[0], yb[1], 0, 0};
+                } else {
+                    x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off);
+                    y = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off);
+                }
+            }
+            kreg[j] = x;
+            vreg[j] = y;
+        }
+    };
+    auto put = [&](uint8_t* buffer) {
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) {
+            const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits, col = u % kUnits;
+            if (kPieces % kTileThreads && u >= kPieces) break;
+            u32x4 x = kreg[j], y = vreg[j];
+            if constexpr (kE5M2) {
+                x = expand(u32x2{x[0], x[1]});
+                y = expand(u32x2{y[0], y[1]});
+            }
+            *reinterpret_cast<u32x4*>(buffer + key * kKeyRow<D> + col * 16) = x;
+            *reinterpret_cast<u32x4*>(buffer + N * kKeyRow<D> + key * kValueRow<D> + col * 16) = y;
+        }
+    };
+
+    int32_t pages = k0 < k1 ? pages_at(k0) : -1, next = -1;
+    if (k0 < k1) {
+        load(k0, pages);
+        next = pages_at(k0 + static_cast<int32_t>(N));
+        put(lds);
+    }
+    uint32_t turn = 0;
+    for (int32_t kb = k0; kb < k1; kb += static_cast<int32_t>(N), turn ^= 1) {
+        const bool more = kb + static_cast<int32_t>(N) < k1;
+        const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
+        const uint8_t* buffer = lds + turn * kBuffer;
+        if (more) {
+            load(kb + static_cast<int32_t>(N), next);
+            pages = next;
+            next = pages_at(kb + 2 * static_cast<int32_t>(N));
+        }
+        __syncthreads();   // this tile is in LDS; the other buffer has been read by every wave
+        if (kb < any_to && kb + static_cast<int32_t>(N) > any_from) {
+            f32x16 s[kSub];
+#pragma unroll
+            for (uint32_t kt = 0; kt < kSub; ++kt) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+#pragma unroll
+                for (uint32_t f = 0; f < kFrags; ++f) {
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(buffer + (32 * kt + c32) * kKeyRow<D> + 32 * f + 16 * half);
+                    s[kt] = mfma32<kE5M2>(x, q[f], s[kt]);
+                }
+            }
+            const bool whole = here == ~0ull && kb >= all_from && kb + static_cast<int32_t>(N) <= all_to;
+            if (!whole) {
+#pragma unroll
+                for (uint32_t kt = 0; kt < kSub; ++kt)
+#pragma unroll
+                    for (uint32_t i = 0; i < 16; ++i) {
+                        const uint32_t key = 32 * kt + 8 * (i / 4) + 4 * half + i % 4;
+                        const int32_t p = kb + static_cast<int32_t>(key);
+                        const bool sees = p >= first && p < last && (here >> key & 1);
+                        s[kt][i] = sees ? s[kt][i] : -kInf;
+                    }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (uint32_t i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+            top = fmaxf(swap32(top, false), swap32(top, true)) * c;
+            const float was = m, now = fmaxf(was, top);
+            const float base = now == -kInf ? 0.f : now;
+            if (__any(now > was)) {
+                const float r = __builtin_amdgcn_exp2f(was - base);
+                l *= r;
+#pragma unroll
+                for (uint32_t d = 0; d < kTiles; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= r;
+            }
+            m = now;
+            u32x4 p[2 * kSub];
+#pragma unroll
+            for (uint32_t kk = 0; kk < 2 * kSub; ++kk) {
+                f32x8 e;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kk / 2][8 * (kk % 2) + i], c, -base));
+                    l += e[i];
+                }
+                p[kk] = pack<kE5M2>(e);
+            }
+            const uint8_t* values = buffer + N * kKeyRow<D>;
+            const uint8_t* read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
+            auto value = [&](uint32_t kk, uint32_t d) {   // V^T operand of keys 16 kk .., elements 32 d ..
+                typedef __attribute__((address_space(3))) i16x4* lds4;
+                const u32x2 lo = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kk * kValueRow<D> + 64 * d)));
+                const u32x2 hi = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + (16 * kk + 8) * kValueRow<D> + 64 * d)));
+                return u32x4{lo[0], lo[1], hi[0], hi[1]};
+            };
+            bool special = false;
+            if (!whole)
+#pragma unroll
+                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
+#pragma unroll
+                    for (uint32_t d = 0; d < kTiles; ++d) special |= not_finite<kE5M2>(value(kk, d));
+            if (!__any(special)) {
+#pragma unroll
+                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
+#pragma unroll
+                    for (uint32_t d = 0; d < kTiles; ++d) o[d] = mfma32<kE5M2>(value(kk, d), p[kk], o[d]);
+            } else {
+                // a weight of 0 would not keep an Inf or NaN that a row does not see out of the product
+#pragma unroll
+                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
+#pragma unroll
+                    for (uint32_t d = 0; d < kTiles; ++d)
+                        o[d] = mfma32<kE5M2>(finite_part<kE5M2>(value(kk, d)), p[kk], o[d]);
+#pragma unroll 1
+                for (uint32_t key = 0; key < N; ++key) {
+                    const int32_t p = kb + static_cast<int32_t>(key);
+                    if (p < first || p >= last || !(here >> key & 1)) continue;
+#pragma unroll
+                    for (uint32_t d = 0; d < kTiles; ++d)
+#pragma unroll
+                        for (uint32_t b = 0; b < 4; ++b) {
+                            float x[4] = {o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
+                            add_not_finite<kE5M2>(
+                                *reinterpret_cast<const u32x2*>(values + key * kValueRow<D> + 64 * d + 16 * b + 8 * half), x);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[d][4 * b + i] = x[i];
+                        }
+                }
+            }
+        }
+        if (more) put(lds + (turn ^ 1) * kBuffer);
+    }
+    if (__any(bad) && lane == 0) flag(a.status);
+
+    const float sum = swap32(l, false) + swap32(l, true);
+    const float base = m == -kInf ? 0.f : m;
+    if (splits <= 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        SZ_GLOBAL uint16_t* to = gptr(a.out) + static_cast<uint64_t>(at.token) * a.out_stride + at.head * D;
+#pragma unroll
+        for (uint32_t d = 0; d < kTiles; ++d) {
+            // a lane has 4 of each 8 elements, its other half the other 4: after
+            // the exchange each has 8 in a row of every other 8
+#pragma unroll
+            for (uint32_t b = 0; b < 2; ++b) {
+                f32x8 y;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = sum == 0.f ? 0.f : o[d][8 * b + i] * inv;
+                const u32x4 w = pack<false>(y);
+                const u32x2 e = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const u32x2 f = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                const uint32_t at8 = 32 * d + 16 * b + 8 * half;
+                if (live && at8 < D) *reinterpret_cast<SZ_GLOBAL u32x4*>(to + at8) = u32x4{e[0], f[0], e[1], f[1]};
+            }
+        }
+        if (live && half == 0) put_lse(a, at, base, sum);
+    } else if (live) {
+        const uint64_t r = (static_cast<uint64_t>(at.token) * (a.group * a.cache.kv_heads) + at.head) * a.splits + blockIdx.y;
+#pragma unroll
+        for (uint32_t d = 0; d < kTiles; ++d)
+#pragma unroll
+            for (uint32_t b = 0; b < 4; ++b) {
+                const uint32_t at4 = 32 * d + 8 * b + 4 * half;
+                if (at4 < D)
+                    *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + at4) =
+                        f32x4{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
+            }
+        if (half == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
+    }
+}
+
 // Joins the splits of each row: one wave a row, D / 64 (or fewer lanes) sums a lane.
 template <uint32_t D>
 __global__ __launch_bounds__(256) void k_join(AttentionArgs a) {
@@ -540,7 +828,8 @@ hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
     const dim3 grid(static_cast<uint32_t>(slots * a.cache.kv_heads), a.splits);
     if (a.tile == 16) k_attend_few<D, kE5M2, 1><<<grid, kFewThreads, 0, s>>>(a);
-    else k_attend_few<D, kE5M2, 2><<<grid, kFewThreads, 0, s>>>(a);
+    else if (a.tile == 32) k_attend_few<D, kE5M2, 2><<<grid, kFewThreads, 0, s>>>(a);
+    else k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
     if (a.splits > 1) {
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
         k_join<D><<<static_cast<uint32_t>((rows + 3) / 4), 256, 0, s>>>(a);
