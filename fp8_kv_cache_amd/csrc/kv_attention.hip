@@ -23,6 +23,8 @@
 // BF16's bits, smaller ones lose less than 2^-38 of the largest.
 #include "kv_internal.h"
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "splitzip.h"
 
@@ -56,6 +58,8 @@ __device__ inline u32x4 expand(u32x2 b) {
     return u32x4{sz::perm(0, b[0], 0x010C000Cu), sz::perm(0, b[0], 0x030C020Cu), sz::perm(0, b[1], 0x010C000Cu),
                  sz::perm(0, b[1], 0x030C020Cu)};
 }
+
+__device__ inline u32x4 expand(u32x4 x) { return x; }   // BF16 is multiplied as it is
 
 template <bool kE5M2>
 __device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -171,26 +175,31 @@ __device__ inline float* part_stats(const AttentionArgs& a) {
 
 // ---- Few rows: tiles of 16 * NT rows, one tile, KV head and split of the
 // keys a workgroup.  Its 4 waves take 32-key blocks in turn, each wave with
-// its own running maximum and sums, joined through LDS at the end.  K comes
-// from global memory straight in the operand's layout (a lane has 16 bytes of
-// one key), V through a wave's own 32-key LDS buffer.
+// its own running maximum and sums, joined through LDS at the end.  A block
+// goes through the wave's own part of LDS: rows are read from memory in one
+// run each, the next block's while this one is multiplied.
 constexpr uint32_t kFewThreads = 256, kFewWaves = 4, kBlockKeys = 32;
 
 template <uint32_t D>
-constexpr uint32_t kRowBytes = 2 * D + (D % 32 ? 0 : 32);   // LDS row of D 16-bit values: 8 dwords modulo 16, no bank conflicts
+constexpr uint32_t kKeyRow = 2 * D + 16;                       // K rows in LDS: 16-byte reads of 16 rows meet all banks
+template <uint32_t D>
+constexpr uint32_t kFewRow = 2 * D + (D % 32 ? 0 : 32);        // V rows: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
+
+template <uint32_t D>
+constexpr uint32_t kFewStage = kBlockKeys * (kKeyRow<D> + kFewRow<D>);   // a wave's K and V block
 
 template <uint32_t D, uint32_t NT>
 constexpr uint32_t few_lds_bytes() {
-    constexpr uint32_t stage = kFewWaves * kBlockKeys * kRowBytes<D>;
+    constexpr uint32_t stage = kFewWaves * kFewStage<D>;
     constexpr uint32_t join = kFewWaves * 16 * (D + 4) * 4;
     return (stage > join ? stage : join) + kFewWaves * 16 * NT * 8;
 }
 
 template <uint32_t D, bool kE5M2, uint32_t NT>
-__global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
+__global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
     constexpr uint32_t M = 16 * NT, kFrags = (D + 31) / 32, kTiles = D / 16, kUnits = D / 8;
-    constexpr uint32_t kPer = kUnits / 2;            // 8-element units of V a lane stages for a block
-    constexpr uint32_t kUnitBytes = kE5M2 ? 8 : 16;
+    constexpr uint32_t kPer = kUnits / 2;            // pieces of K, and of V, a lane has of a block
+    typedef typename std::conditional<kE5M2, u32x2, u32x4>::type Piece;
     __shared__ __align__(16) uint8_t lds[few_lds_bytes<D, NT>()];
     const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
     const uint64_t slot = blockIdx.x / a.cache.kv_heads;
@@ -255,7 +264,8 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
         for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    uint8_t* stage = lds + wave * (kBlockKeys * kRowBytes<D>);
+    uint8_t* keys = lds + wave * kFewStage<D>;
+    uint8_t* values = keys + kBlockKeys * kKeyRow<D>;
     const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
     const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
     bool bad = false;
@@ -268,47 +278,20 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
         bad |= page < 0;
         return page;
     };
-    u32x4 kreg[2][kFrags], vreg[kPer];
-    auto load_k = [&](int32_t kb, int32_t pages) {
-#pragma unroll
-        for (uint32_t kt = 0; kt < 2; ++kt) {
-            const int32_t page = __shfl(pages, kt * 16 + c16);
-            const SZ_GLOBAL uint8_t* from = pool_k;
-            if (page >= 0) from += slot_offset(a.cache, page, kb + static_cast<int32_t>(kt * 16 + c16));
-#pragma unroll
-            for (uint32_t f = 0; f < kFrags; ++f) {
-                u32x4 x = u32x4{0, 0, 0, 0};
-                if (page >= 0 && 32 * f + 8 * g < D) {
-                    if constexpr (kE5M2) {
-                        const u32x2 b = *reinterpret_cast<const SZ_GLOBAL u32x2*>(from + 32 * f + 8 * g);
-                        x[0] = b[0];
-                        x[1] = b[1];
-                    } else {
-                        x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 2 * (32 * f + 8 * g));
-                    }
-                }
-                kreg[kt][f] = x;
-            }
-        }
-    };
-    auto load_v = [&](int32_t kb, int32_t pages) {
+    // Piece j of a lane: 8 elements of key u / kUnits, neighbouring lanes
+    // along the key, so that a row is read in one run.
+    Piece kreg[kPer], vreg[kPer];
+    auto load = [&](int32_t kb, int32_t pages) {
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
-            const uint32_t u = lane + 64 * j, row = u / kUnits, col = u % kUnits;
-            const int32_t page = __shfl(pages, row);
-            u32x4 x = u32x4{0, 0, 0, 0};
+            const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
+            const int32_t page = __shfl(pages, key);
+            kreg[j] = vreg[j] = Piece{};
             if (page >= 0) {
-                const SZ_GLOBAL uint8_t* from =
-                    pool_v + slot_offset(a.cache, page, kb + static_cast<int32_t>(row)) + col * kUnitBytes;
-                if constexpr (kE5M2) {
-                    const u32x2 b = *reinterpret_cast<const SZ_GLOBAL u32x2*>(from);
-                    x[0] = b[0];
-                    x[1] = b[1];
-                } else {
-                    x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(from);
-                }
+                const uint64_t off = slot_offset(a.cache, page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
+                kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off));
+                vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off));
             }
-            vreg[j] = x;
         }
     };
 
@@ -317,12 +300,25 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
     int32_t pages = -1, next_pages = -1;
     if (kb < k1) {
         pages = pages_at(kb);
-        load_k(kb, pages);
-        load_v(kb, pages);
+        load(kb, pages);
         if (kb + step < k1) next_pages = pages_at(kb + step);
     }
     for (; kb < k1; kb += step) {
         const bool more = kb + step < k1;
+        const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
+        wave_lds_order();
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) {
+            const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
+            *reinterpret_cast<u32x4*>(keys + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
+            *reinterpret_cast<u32x4*>(values + key * kFewRow<D> + col * 16) = expand(vreg[j]);
+        }
+        wave_lds_order();
+        if (more) {
+            load(kb + step, next_pages);
+            pages = next_pages;
+            next_pages = kb + 2 * step < k1 ? pages_at(kb + 2 * step) : -1;
+        }
         f32x4 s[NT][2];
 #pragma unroll
         for (uint32_t kt = 0; kt < 2; ++kt) {
@@ -330,32 +326,16 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
             for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (uint32_t f = 0; f < kFrags; ++f) {
-                u32x4 x = kreg[kt][f];
-                if constexpr (kE5M2) x = expand(u32x2{x[0], x[1]});
+                // past the row's end (D = 80) Q is 0, and K must be too: LDS holds anything there
+                u32x4 x = *reinterpret_cast<const u32x4*>(keys + (16 * kt + c16) * kKeyRow<D> + 64 * f + 16 * g);
+                if (32 * f + 32 > D && 32 * f + 8 * g >= D) x = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = mfma16<kE5M2>(x, q[nt][f], s[nt][kt]);
             }
         }
-        wave_lds_order();
-#pragma unroll
-        for (uint32_t j = 0; j < kPer; ++j) {
-            const uint32_t u = lane + 64 * j, row = u / kUnits, col = u % kUnits;
-            u32x4 x = vreg[j];
-            if constexpr (kE5M2) x = expand(u32x2{x[0], x[1]});
-            *reinterpret_cast<u32x4*>(stage + row * kRowBytes<D> + col * 16) = x;
-        }
-        wave_lds_order();
-        const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
-        const int32_t this_pages_ok = static_cast<uint32_t>(here) == 0xFFFFFFFFu;
-        if (more) {
-            load_k(kb + step, next_pages);
-            load_v(kb + step, next_pages);
-            pages = next_pages;
-            next_pages = kb + 2 * step < k1 ? pages_at(kb + 2 * step) : -1;
-        }
 
         // every row sees every key of the block?
-        const bool whole = this_pages_ok && kb >= a.mask.first(t.p1) &&
+        const bool whole = here == ~0ull && kb >= a.mask.first(t.p1) &&
                            kb + static_cast<int32_t>(kBlockKeys) <= a.mask.last(t.p0, t.seq.kv);
         u32x4 p[NT];
 #pragma unroll
@@ -393,12 +373,12 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
             p[nt] = pack<kE5M2>(e);
         }
 
-        const uint8_t* read = stage + (4 * g + c16 / 4) * kRowBytes<D> + c16 % 4 * 8;
+        const uint8_t* read = values + (4 * g + c16 / 4) * kFewRow<D> + c16 % 4 * 8;
         auto value = [&](uint32_t d) {   // V^T operand of elements 16 d ..
             typedef __attribute__((address_space(3))) i16x4* lds4;
             const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + d * 32)));
             const u32x2 hi = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kRowBytes<D> + d * 32)));
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kFewRow<D> + d * 32)));
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         };
         bool special = false;
@@ -429,7 +409,7 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
 #pragma unroll
                     for (uint32_t d = 0; d < kTiles; ++d) {
                         float x[4] = {o[nt][d][0], o[nt][d][1], o[nt][d][2], o[nt][d][3]};
-                        add_not_finite<kE5M2>(*reinterpret_cast<const u32x2*>(stage + key * kRowBytes<D> + 32 * d + 8 * g), x);
+                        add_not_finite<kE5M2>(*reinterpret_cast<const u32x2*>(values + key * kFewRow<D> + 32 * d + 8 * g), x);
                         o[nt][d] = f32x4{x[0], x[1], x[2], x[3]};
                     }
                 }
@@ -499,8 +479,6 @@ __global__ __launch_bounds__(kFewThreads) void k_attend_few(AttentionArgs a) {
 // is multiplied, and are put into the other buffer behind it.
 constexpr uint32_t kTileThreads = 256, kTileRows = 128;
 
-template <uint32_t D>
-constexpr uint32_t kKeyRow = 2 * D + 16;                          // K rows in LDS: 16-byte reads of 16 rows meet all banks
 template <uint32_t D>
 constexpr uint32_t kValueRow = ((2 * D + 63) / 64 | 1) * 64;      // V rows: 4 rows of 64 bytes meet all banks
 
