@@ -47,6 +47,20 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
 
+// Pointers into LDS stay in its address space: a cast from a generic pointer
+// costs a null check at every use.
+#define KV_LDS __attribute__((address_space(3)))
+typedef KV_LDS uint8_t* LdsBytes;
+template <typename T>
+__device__ inline KV_LDS T* lds_as(LdsBytes p) {
+    return (KV_LDS T*)p;
+}
+// 4 x 16 transposing read: 16 lanes give the addresses of 4 rows of 32 bytes
+// (4 lanes a row), lane i gets element i of each row
+__device__ inline u32x2 read_tr16(LdsBytes p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_as<i16x4>(p)));
+}
+
 __device__ inline void flag(int32_t* status) {
     if (status) *gptr(status) = SZ_ERR_INVALID_ARGUMENT;
 }
@@ -148,6 +162,24 @@ __device__ inline void wave_lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// The tile of a workgroup, its fields in scalar registers.
+__device__ inline Tile my_tile(const AttentionArgs& a, uint64_t slot, uint32_t M) {
+    Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    auto scalar = [](int32_t& x) { x = __builtin_amdgcn_readfirstlane(x); };
+    scalar(t.seq.begin);
+    scalar(t.seq.n);
+    scalar(t.seq.kv);
+    scalar(t.seen);
+    scalar(t.lo);
+    scalar(t.hi);
+    scalar(t.p0);
+    scalar(t.p1);
+    t.s = uniform(t.s);
+    t.row0 = uniform(t.row0);
+    t.rows = uniform(t.rows);
+    return t;
+}
+
 // Query row `row` of the tile's sequence: its token and head.
 struct RowAt {
     uint32_t token;   // row of the per-token tensors
@@ -206,7 +238,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
         !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
         flag(a.status);
-    const Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    const Tile t = my_tile(a, slot, M);
     if (!t.any) return;
     const uint32_t splits = splits_of(t, a.split_len);
     if (blockIdx.y && blockIdx.y >= splits) return;
@@ -264,13 +296,14 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
         for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    uint8_t* keys = lds + wave * kFewStage<D>;
-    uint8_t* values = keys + kBlockKeys * kKeyRow<D>;
+    const LdsBytes keys = (LdsBytes)lds + wave * kFewStage<D>;
+    const LdsBytes values = keys + kBlockKeys * kKeyRow<D>;
     const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
     const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
     bool bad = false;
 
-    // page of the block's key `lane % 32`, or -1
+    // page of the block's key `lane % 32`, or -1.  Keys without a page are
+    // loaded from page 0: their scores are masked, their values get weight 0.
     auto pages_at = [&](int32_t kb) -> int32_t {
         const int32_t p = kb + static_cast<int32_t>(lane % kBlockKeys);
         if (p < t.seen || p >= k1) return -1;
@@ -286,12 +319,10 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
             const int32_t page = __shfl(pages, key);
-            kreg[j] = vreg[j] = Piece{};
-            if (page >= 0) {
-                const uint64_t off = slot_offset(a.cache, page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
-                kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off));
-                vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off));
-            }
+            const uint64_t off =
+                slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
+            kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off));
+            vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off));
         }
     };
 
@@ -310,8 +341,8 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
-            *reinterpret_cast<u32x4*>(keys + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
-            *reinterpret_cast<u32x4*>(values + key * kFewRow<D> + col * 16) = expand(vreg[j]);
+            *lds_as<u32x4>(keys + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
+            *lds_as<u32x4>(values + key * kFewRow<D> + col * 16) = expand(vreg[j]);
         }
         wave_lds_order();
         if (more) {
@@ -327,7 +358,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
 #pragma unroll
             for (uint32_t f = 0; f < kFrags; ++f) {
                 // past the row's end (D = 80) Q is 0, and K must be too: LDS holds anything there
-                u32x4 x = *reinterpret_cast<const u32x4*>(keys + (16 * kt + c16) * kKeyRow<D> + 64 * f + 16 * g);
+                u32x4 x = *lds_as<u32x4>(keys + (16 * kt + c16) * kKeyRow<D> + 64 * f + 16 * g);
                 if (32 * f + 32 > D && 32 * f + 8 * g >= D) x = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = mfma16<kE5M2>(x, q[nt][f], s[nt][kt]);
@@ -337,6 +368,8 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
         // every row sees every key of the block?
         const bool whole = here == ~0ull && kb >= a.mask.first(t.p1) &&
                            kb + static_cast<int32_t>(kBlockKeys) <= a.mask.last(t.p0, t.seq.kv);
+        const int32_t kb4 = kb + static_cast<int32_t>(4 * g);
+        const uint32_t mine = static_cast<uint32_t>(here >> (4 * g));
         u32x4 p[NT];
 #pragma unroll
         for (uint32_t nt = 0; nt < NT; ++nt) {
@@ -345,9 +378,9 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
                 for (uint32_t kt = 0; kt < 2; ++kt)
 #pragma unroll
                     for (uint32_t j = 0; j < 4; ++j) {
-                        const uint32_t key = 16 * kt + 4 * g + j;
-                        const int32_t at = kb + static_cast<int32_t>(key);
-                        const bool sees = at >= first[nt] && at < last[nt] && (here >> key & 1);
+                        // key 16 kt + 4 g + j
+                        const int32_t i = static_cast<int32_t>(16 * kt + j);
+                        const bool sees = i >= first[nt] - kb4 && i < last[nt] - kb4 && (mine >> i & 1);
                         s[nt][kt][j] = sees ? s[nt][kt][j] : -kInf;
                     }
             }
@@ -373,12 +406,9 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
             p[nt] = pack<kE5M2>(e);
         }
 
-        const uint8_t* read = values + (4 * g + c16 / 4) * kFewRow<D> + c16 % 4 * 8;
+        const LdsBytes read = values + (4 * g + c16 / 4) * kFewRow<D> + c16 % 4 * 8;
         auto value = [&](uint32_t d) {   // V^T operand of elements 16 d ..
-            typedef __attribute__((address_space(3))) i16x4* lds4;
-            const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + d * 32)));
-            const u32x2 hi = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kFewRow<D> + d * 32)));
+            const u32x2 lo = read_tr16(read + d * 32), hi = read_tr16(read + 16 * kFewRow<D> + d * 32);
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         };
         bool special = false;
@@ -409,7 +439,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
 #pragma unroll
                     for (uint32_t d = 0; d < kTiles; ++d) {
                         float x[4] = {o[nt][d][0], o[nt][d][1], o[nt][d][2], o[nt][d][3]};
-                        add_not_finite<kE5M2>(*reinterpret_cast<const u32x2*>(values + key * kFewRow<D> + 32 * d + 8 * g), x);
+                        add_not_finite<kE5M2>(*lds_as<u32x2>(values + key * kFewRow<D> + 32 * d + 8 * g), x);
                         o[nt][d] = f32x4{x[0], x[1], x[2], x[3]};
                     }
                 }
@@ -493,7 +523,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
         !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
         flag(a.status);
-    const Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    const Tile t = my_tile(a, slot, M);
     if (!t.any) return;
     const uint32_t splits = splits_of(t, a.split_len);
     if (blockIdx.y && blockIdx.y >= splits) return;
@@ -559,41 +589,26 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
         bad |= page < 0;
         return page;
     };
-    u32x4 kreg[kPer], vreg[kPer];
+    typedef typename std::conditional<kE5M2, u32x2, u32x4>::type Piece;
+    Piece kreg[kPer], vreg[kPer];
     auto load = [&](int32_t kb, int32_t pages) {
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
-            const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits, col = u % kUnits;
-            const int32_t page = __shfl(pages, key % 64);
-            u32x4 x = u32x4{0, 0, 0, 0}, y = x;
-            if (page >= 0 && u < kPieces) {
-                const uint64_t off = slot_offset(a.cache, page, kb + static_cast<int32_t>(key)) + col * (kE5M2 ? 8 : 16);
-                if constexpr (kE5M2) {
-                    const u32x2 xb = *reinterpret_cast<const SZ_GLOBAL u32x2*>(pool_k + off);
-                    const u32x2 yb = *reinterpret_cast<const SZ_GLOBAL u32x2*>(pool_v + off);
-                    x = u32x4{xb[0], xb[1], 0, 0};
-                    y = u32x4{yb[0], yb[1], 0, 0};
-                } else {
-                    x = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off);
-                    y = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off);
-                }
-            }
-            kreg[j] = x;
-            vreg[j] = y;
+            const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits % N, col = u % kUnits;
+            const int32_t page = __shfl(pages, key);
+            const uint64_t off =
+                slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
+            kreg[j] = *reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off);
+            vreg[j] = *reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off);
         }
     };
-    auto put = [&](uint8_t* buffer) {
+    auto put = [&](LdsBytes buffer) {
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits, col = u % kUnits;
             if (kPieces % kTileThreads && u >= kPieces) break;
-            u32x4 x = kreg[j], y = vreg[j];
-            if constexpr (kE5M2) {
-                x = expand(u32x2{x[0], x[1]});
-                y = expand(u32x2{y[0], y[1]});
-            }
-            *reinterpret_cast<u32x4*>(buffer + key * kKeyRow<D> + col * 16) = x;
-            *reinterpret_cast<u32x4*>(buffer + N * kKeyRow<D> + key * kValueRow<D> + col * 16) = y;
+            *lds_as<u32x4>(buffer + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
+            *lds_as<u32x4>(buffer + N * kKeyRow<D> + key * kValueRow<D> + col * 16) = expand(vreg[j]);
         }
     };
 
@@ -601,18 +616,19 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     if (k0 < k1) {
         load(k0, pages);
         next = pages_at(k0 + static_cast<int32_t>(N));
-        put(lds);
+        put((LdsBytes)lds);
     }
     uint32_t turn = 0;
     for (int32_t kb = k0; kb < k1; kb += static_cast<int32_t>(N), turn ^= 1) {
         const bool more = kb + static_cast<int32_t>(N) < k1;
         const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
-        const uint8_t* buffer = lds + turn * kBuffer;
-        if (more) {
+        const LdsBytes buffer = (LdsBytes)lds + turn * kBuffer;
+        auto fetch = [&] {
+            if (!more) return;
             load(kb + static_cast<int32_t>(N), next);
             pages = next;
             next = pages_at(kb + 2 * static_cast<int32_t>(N));
-        }
+        };
         __syncthreads();   // this tile is in LDS; the other buffer has been read by every wave
         if (kb < any_to && kb + static_cast<int32_t>(N) > any_from) {
             f32x16 s[kSub];
@@ -622,21 +638,25 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                 for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
                 for (uint32_t f = 0; f < kFrags; ++f) {
-                    const u32x4 x = *reinterpret_cast<const u32x4*>(buffer + (32 * kt + c32) * kKeyRow<D> + 32 * f + 16 * half);
+                    const u32x4 x = *lds_as<u32x4>(buffer + (32 * kt + c32) * kKeyRow<D> + 32 * f + 16 * half);
                     s[kt] = mfma32<kE5M2>(x, q[f], s[kt]);
                 }
             }
+            fetch();   // behind the first product: its registers are then free
             const bool whole = here == ~0ull && kb >= all_from && kb + static_cast<int32_t>(N) <= all_to;
             if (!whole) {
+                const int32_t from = first - kb - static_cast<int32_t>(4 * half), to = last - kb - static_cast<int32_t>(4 * half);
 #pragma unroll
-                for (uint32_t kt = 0; kt < kSub; ++kt)
+                for (uint32_t kt = 0; kt < kSub; ++kt) {
+                    const uint32_t mine = static_cast<uint32_t>(here >> (32 * kt)) >> (4 * half);
 #pragma unroll
                     for (uint32_t i = 0; i < 16; ++i) {
-                        const uint32_t key = 32 * kt + 8 * (i / 4) + 4 * half + i % 4;
-                        const int32_t p = kb + static_cast<int32_t>(key);
-                        const bool sees = p >= first && p < last && (here >> key & 1);
+                        const int32_t key = static_cast<int32_t>(8 * (i / 4) + i % 4);   // and 32 kt + 4 half
+                        const bool sees = key + static_cast<int32_t>(32 * kt) >= from && key + static_cast<int32_t>(32 * kt) < to &&
+                                          (mine >> key & 1);
                         s[kt][i] = sees ? s[kt][i] : -kInf;
                     }
+                }
             }
             float top = s[0][0];
 #pragma unroll
@@ -664,14 +684,11 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                 }
                 p[kk] = pack<kE5M2>(e);
             }
-            const uint8_t* values = buffer + N * kKeyRow<D>;
-            const uint8_t* read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
+            const LdsBytes values = buffer + N * kKeyRow<D>;
+            const LdsBytes read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
             auto value = [&](uint32_t kk, uint32_t d) {   // V^T operand of keys 16 kk .., elements 32 d ..
-                typedef __attribute__((address_space(3))) i16x4* lds4;
-                const u32x2 lo = __builtin_bit_cast(
-                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + 16 * kk * kValueRow<D> + 64 * d)));
-                const u32x2 hi = __builtin_bit_cast(
-                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(read + (16 * kk + 8) * kValueRow<D> + 64 * d)));
+                const u32x2 lo = read_tr16(read + 16 * kk * kValueRow<D> + 64 * d);
+                const u32x2 hi = read_tr16(read + (16 * kk + 8) * kValueRow<D> + 64 * d);
                 return u32x4{lo[0], lo[1], hi[0], hi[1]};
             };
             bool special = false;
@@ -702,14 +719,16 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                         for (uint32_t b = 0; b < 4; ++b) {
                             float x[4] = {o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
                             add_not_finite<kE5M2>(
-                                *reinterpret_cast<const u32x2*>(values + key * kValueRow<D> + 64 * d + 16 * b + 8 * half), x);
+                                *lds_as<u32x2>(values + key * kValueRow<D> + 64 * d + 16 * b + 8 * half), x);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) o[d][4 * b + i] = x[i];
                         }
                 }
             }
+        } else {
+            fetch();
         }
-        if (more) put(lds + (turn ^ 1) * kBuffer);
+        if (more) put((LdsBytes)lds + (turn ^ 1) * kBuffer);
     }
     if (__any(bad) && lane == 0) flag(a.status);
 
