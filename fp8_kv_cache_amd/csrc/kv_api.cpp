@@ -233,7 +233,7 @@ kvi::AttentionPlan kvi::attention_plan(uint32_t kv_heads, uint32_t group, uint32
                                        uint32_t window) {
     AttentionPlan p{};
     const uint64_t most_rows = static_cast<uint64_t>(max_tokens) * group;
-    p.tile = most_rows <= 16 ? 16 : most_rows <= 64 ? 32 : 128;
+    p.tile = most_rows <= 16 ? 16 : 128;
     // positions that a tile can see, and tiles that the call can have
     uint64_t range = max_kv_len;
     if (window && static_cast<uint64_t>(window) + p.tile + 32 < range) range = static_cast<uint64_t>(window) + p.tile + 32;
@@ -241,7 +241,7 @@ kvi::AttentionPlan kvi::attention_plan(uint32_t kv_heads, uint32_t group, uint32
     const uint64_t rows = static_cast<uint64_t>(total_tokens) * group;
     const uint64_t tiles = (rows / p.tile + (rows / p.tile < num_seqs ? rows / p.tile : num_seqs) + 1) * kv_heads;
     // Enough workgroups to fill the GPU, each with at least 256 positions.
-    constexpr uint64_t kGroups = 1024, kLeast = 256;
+    const uint64_t kGroups = p.tile == 128 ? 512 : 1024, kLeast = 256;
     uint64_t splits = tiles < kGroups ? (kGroups + tiles - 1) / tiles : 1;
     const uint64_t most = (range + kLeast - 1) / kLeast;
     if (splits > most) splits = most;

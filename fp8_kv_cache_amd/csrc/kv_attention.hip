@@ -61,6 +61,12 @@ __device__ inline u32x2 read_tr16(LdsBytes p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_as<i16x4>(p)));
 }
 
+// 8 x 16 transposing read of bytes: 2 lanes a row
+__device__ inline u32x2 read_tr8(LdsBytes p) {
+    typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(lds_as<i32x2>(p)));
+}
+
 __device__ inline void flag(int32_t* status) {
     if (status) *gptr(status) = SZ_ERR_INVALID_ARGUMENT;
 }
@@ -72,8 +78,6 @@ __device__ inline u32x4 expand(u32x2 b) {
     return u32x4{sz::perm(0, b[0], 0x010C000Cu), sz::perm(0, b[0], 0x030C020Cu), sz::perm(0, b[1], 0x010C000Cu),
                  sz::perm(0, b[1], 0x030C020Cu)};
 }
-
-__device__ inline u32x4 expand(u32x4 x) { return x; }   // BF16 is multiplied as it is
 
 template <bool kE5M2>
 __device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -117,33 +121,42 @@ __device__ inline float row_sum(float x) {
     return swap32(x, false) + swap32(x, true);
 }
 
-// Whether any of 8 packed 16-bit values is Inf or NaN.
+// A 16-byte piece of a value row as the cache holds it: whether it has Inf or
+// NaN, and the piece with 0 in their places.
 template <bool kE5M2>
 __device__ inline bool not_finite(u32x4 x) {
-    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u;
     bool any = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        any |= (x[i] & kExp) == kExp || (x[i] & (kExp << 16)) == (kExp << 16);
+#pragma unroll
+        for (int h = 0; h < 32; h += kE5M2 ? 8 : 16) {
+            const uint32_t kExp = (kE5M2 ? 0x7Cu : 0x7F80u) << h;
+            any |= (x[i] & kExp) == kExp;
+        }
     return any;
 }
-
-// 8 packed values with 0 for the Inf and NaN among them.
 template <bool kE5M2>
 __device__ inline u32x4 finite_part(u32x4 x) {
-    constexpr uint32_t kExp = kE5M2 ? 0x7C00u : 0x7F80u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = (x[i] & kExp) == kExp ? 0u : x[i] & 0xFFFFu;
-        const uint32_t hi = (x[i] & (kExp << 16)) == (kExp << 16) ? 0u : x[i] & 0xFFFF0000u;
-        x[i] = lo | hi;
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 32; h += kE5M2 ? 8 : 16) {
+            const uint32_t kExp = (kE5M2 ? 0x7Cu : 0x7F80u) << h;
+            if ((x[i] & kExp) == kExp) x[i] &= ~((kE5M2 ? 0xFFu : 0xFFFFu) << h);
+        }
     return x;
 }
 
-// Adds the Inf and NaN among 4 packed values to 4 sums.
+// Adds the Inf and NaN among the 4 values at `from` to 4 sums.
 template <bool kE5M2>
-__device__ inline void add_not_finite(u32x2 x, float* o) {
+__device__ inline void add_not_finite(const SZ_GLOBAL uint8_t* from, float* o) {
+    u32x2 x;   // BF16, or the E5M2 bytes as FP16
+    if constexpr (kE5M2) {
+        const uint32_t b = *reinterpret_cast<const SZ_GLOBAL uint32_t*>(from);
+        x = u32x2{sz::perm(0, b, 0x010C000Cu), sz::perm(0, b, 0x030C020Cu)};
+    } else {
+        x = *reinterpret_cast<const SZ_GLOBAL u32x2*>(from);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t v = x[i / 2] >> (i % 2 * 16) & 0xFFFFu;
@@ -154,6 +167,10 @@ __device__ inline void add_not_finite(u32x2 x, float* o) {
         }
     }
 }
+
+// How far a row's maximum may pass the one its sums are scaled by before
+// they are rescaled: the weights stay below 2^8, exact in every type here.
+constexpr float kSlack = 8.f;
 
 // LDS order inside one wave: its LDS instructions execute in order; this
 // keeps the compiler from moving one lane's reads over another's writes.
@@ -180,6 +197,30 @@ __device__ inline Tile my_tile(const AttentionArgs& a, uint64_t slot, uint32_t M
     return t;
 }
 
+// The page ids of a block's keys, a key a lane.  `ask` only loads (an entry
+// that exists, whatever the position), so that nothing waits for it before
+// `answer` a block later: -1 where the position has no page, or is outside
+// [seen, end) and so none is needed.
+struct Pages {
+    const SZ_GLOBAL int32_t* row;
+    uint32_t log2_page, last, num_pages;
+    int32_t seen, end;
+    bool bad;
+    __device__ Pages(const AttentionArgs& a, const Tile& t, int32_t k1)
+        : row(gptr(a.batch.pages) + t.s * a.batch.pages_stride), log2_page(a.cache.log2_page),
+          last(a.batch.pages_per_seq - 1), num_pages(a.cache.num_pages), seen(t.seen), end(k1), bad(false) {}
+    __device__ int32_t ask(int32_t p) const {
+        const uint32_t i = static_cast<uint32_t>(p) >> log2_page;
+        return row[i < last ? i : last];
+    }
+    __device__ int32_t answer(int32_t p, int32_t id) {
+        if (p < seen || p >= end) return -1;
+        const bool ok = static_cast<uint32_t>(p) >> log2_page <= last && static_cast<uint32_t>(id) < num_pages;
+        bad |= !ok;
+        return ok ? id : -1;
+    }
+};
+
 // Query row `row` of the tile's sequence: its token and head.
 struct RowAt {
     uint32_t token;   // row of the per-token tensors
@@ -205,40 +246,76 @@ __device__ inline float* part_stats(const AttentionArgs& a) {
     return a.part + rows * a.splits * a.cache.head_dim;
 }
 
-// ---- Few rows: tiles of 16 * NT rows, one tile, KV head and split of the
-// keys a workgroup.  Its 4 waves take 32-key blocks in turn, each wave with
-// its own running maximum and sums, joined through LDS at the end.  A block
-// goes through the wave's own part of LDS: rows are read from memory in one
-// run each, the next block's while this one is multiplied.
-constexpr uint32_t kFewThreads = 256, kFewWaves = 4, kBlockKeys = 32;
-
-template <uint32_t D>
-constexpr uint32_t kKeyRow = 2 * D + 16;                       // K rows in LDS: 16-byte reads of 16 rows meet all banks
-template <uint32_t D>
-constexpr uint32_t kFewRow = 2 * D + (D % 32 ? 0 : 32);        // V rows: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
-
-template <uint32_t D>
-constexpr uint32_t kFewStage = kBlockKeys * (kKeyRow<D> + kFewRow<D>);   // a wave's K and V block
-
-template <uint32_t D, uint32_t NT>
-constexpr uint32_t few_lds_bytes() {
-    constexpr uint32_t stage = kFewWaves * kFewStage<D>;
-    constexpr uint32_t join = kFewWaves * 16 * (D + 4) * 4;
-    return (stage > join ? stage : join) + kFewWaves * 16 * NT * 8;
+// A query row's operands from BF16 to FP16, scaled by the power of two that
+// brings its largest element to [2^14, 2^15); returns c scaled back.
+template <uint32_t kFrags, typename Max>
+__device__ inline float to_fp16(u32x4* q, float c, Max over_row) {
+    float most = 0.f;
+#pragma unroll
+    for (uint32_t f = 0; f < kFrags; ++f) {
+        const f32x8 x = to_f32(q[f]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
+    }
+    most = over_row(most);
+    const int32_t up = most > 0.f && most < kInf ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
+#pragma unroll
+    for (uint32_t f = 0; f < kFrags; ++f) {
+        f32x8 x = to_f32(q[f]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_ldexpf(x[j], up);
+        q[f] = pack<true>(x);
+    }
+    return __builtin_amdgcn_ldexpf(c, -up);
 }
 
-template <uint32_t D, bool kE5M2, uint32_t NT>
+// Asks the scheduler to keep kAhead operands' LDS reads (kReads each) in
+// flight before each of the block's kCount matrix instructions: left alone it
+// reads an operand right before its use and waits for LDS every time.
+template <uint32_t kCount, uint32_t kReads, uint32_t kAhead>
+__device__ inline void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, kReads * kAhead, 0);
+#pragma unroll
+    for (uint32_t i = 0; i < kCount; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i + kAhead < kCount) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+    }
+}
+
+// ---- Few rows: tiles of 16 rows, one tile, KV head and split of the keys a
+// workgroup.  Its 4 waves take blocks of keys in turn, each wave with its own
+// running maximum and sums, joined through LDS at the end.  A block goes
+// through the wave's own part of LDS as the cache has it: rows are read from
+// memory in one run each, the next block's while this one is multiplied.
+constexpr uint32_t kFewThreads = 256, kFewWaves = 4;
+
+template <uint32_t D>
+constexpr uint32_t kKeyRow = 2 * D + 16;   // rows of 16-bit K in LDS: 16-byte reads of 16 rows meet all banks
+
+template <uint32_t D, bool kE5M2>
+struct Few {
+    static constexpr uint32_t kKeys = kE5M2 ? 64 : 32;   // a block: 16 KB of K and V either way at D = 128
+    static constexpr uint32_t kSize = kE5M2 ? 1 : 2;
+    // rows in LDS; BF16 V: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
+    static constexpr uint32_t kK = D * kSize + 16, kV = kE5M2 ? D + 16 : 2 * D + (D % 32 ? 0 : 32);
+    static constexpr uint32_t kStage = kKeys * (kK + kV);
+    static constexpr uint32_t kJoin = 16 * (D + 4) * 4;
+    static constexpr uint32_t kLds = kFewWaves * ((kStage > kJoin ? kStage : kJoin) + 16 * 8);
+};
+
+template <uint32_t D, bool kE5M2>
 __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
-    constexpr uint32_t M = 16 * NT, kFrags = (D + 31) / 32, kTiles = D / 16, kUnits = D / 8;
-    constexpr uint32_t kPer = kUnits / 2;            // pieces of K, and of V, a lane has of a block
-    typedef typename std::conditional<kE5M2, u32x2, u32x4>::type Piece;
-    __shared__ __align__(16) uint8_t lds[few_lds_bytes<D, NT>()];
+    typedef Few<D, kE5M2> F;
+    constexpr uint32_t kKeys = F::kKeys, kSub = kKeys / 16, kFrags = (D + 31) / 32, kTiles = D / 16;
+    constexpr uint32_t kUnits = D * F::kSize / 16;   // 16-byte pieces of a row
+    constexpr uint32_t kPer = kKeys * kUnits / 64;   // pieces of K, and of V, a lane has of a block
+    __shared__ __align__(16) uint8_t lds[F::kLds];
     const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
     const uint64_t slot = blockIdx.x / a.cache.kv_heads;
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
         !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
         flag(a.status);
-    const Tile t = my_tile(a, slot, M);
+    const Tile t = my_tile(a, slot, 16);
     if (!t.any) return;
     const uint32_t splits = splits_of(t, a.split_len);
     if (blockIdx.y && blockIdx.y >= splits) return;
@@ -247,258 +324,208 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
 
     const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16, c16 = lane % 16;
 
-    // Q^T operands: row c16 of each 16-row tile, elements 32 f + 8 g ..
-    u32x4 q[NT][kFrags];
-    float c[NT];
-    int32_t first[NT], last[NT];   // what the lane's row sees
+    // Q^T operands: the lane's row c16, elements 32 f + 8 g ..
+    const bool live = c16 < t.rows;
+    const RowAt at = row_at(t, t.row0 + (live ? c16 : 0), a.group, kv_head);
+    const int32_t first = live ? a.mask.first(at.p) : 0, last = live ? a.mask.last(at.p, t.seq.kv) : 0;
+    u32x4 q[kFrags];
+    const SZ_GLOBAL uint16_t* from = gptr(a.q) + static_cast<uint64_t>(at.token) * a.q_stride + at.head * D;
 #pragma unroll
-    for (uint32_t nt = 0; nt < NT; ++nt) {
-        const uint32_t row = 16 * nt + c16;
-        const bool live = row < t.rows;
-        const RowAt r = row_at(t, t.row0 + (live ? row : 0), a.group, kv_head);
-        first[nt] = live ? a.mask.first(r.p) : 0;
-        last[nt] = live ? a.mask.last(r.p, t.seq.kv) : 0;
-        const SZ_GLOBAL uint16_t* from = gptr(a.q) + static_cast<uint64_t>(r.token) * a.q_stride + r.head * D;
-#pragma unroll
-        for (uint32_t f = 0; f < kFrags; ++f)
-            q[nt][f] = live && 32 * f + 8 * g < D ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 32 * f + 8 * g)
-                                                  : u32x4{0, 0, 0, 0};
-        c[nt] = a.scale * kLog2e;
-        if constexpr (kE5M2) {
-            float most = 0.f;
-#pragma unroll
-            for (uint32_t f = 0; f < kFrags; ++f) {
-                const f32x8 x = to_f32(q[nt][f]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
-            }
-            most = row_max(most);
-            const int32_t up = most > 0.f && most < kInf ? 14 - __builtin_amdgcn_frexp_expf(most) + 1 : 0;
-#pragma unroll
-            for (uint32_t f = 0; f < kFrags; ++f) {
-                f32x8 x = to_f32(q[nt][f]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_ldexpf(x[j], up);
-                q[nt][f] = pack<true>(x);
-            }
-            c[nt] = __builtin_amdgcn_ldexpf(c[nt], -up);
-        }
-        c[nt] = fmaxf(c[nt], 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
-    }
+    for (uint32_t f = 0; f < kFrags; ++f)
+        q[f] = live && 32 * f + 8 * g < D ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 32 * f + 8 * g)
+                                          : u32x4{0, 0, 0, 0};
+    float c = a.scale * kLog2e;
+    if constexpr (kE5M2) c = to_fp16<kFrags>(q, c, [](float x) { return row_max(x); });
+    c = fmaxf(c, 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
 
-    f32x4 o[NT][kTiles];
-    float m[NT], l[NT];
+    f32x4 o[kTiles];
 #pragma unroll
-    for (uint32_t nt = 0; nt < NT; ++nt) {
-        m[nt] = -kInf;
-        l[nt] = 0.f;
-#pragma unroll
-        for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (uint32_t d = 0; d < kTiles; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -kInf, l = 0.f;
 
-    const LdsBytes keys = (LdsBytes)lds + wave * kFewStage<D>;
-    const LdsBytes values = keys + kBlockKeys * kKeyRow<D>;
+    const LdsBytes keys = (LdsBytes)lds + wave * F::kStage;
+    const LdsBytes values = keys + kKeys * F::kK;
     const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
     const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
-    bool bad = false;
+    Pages table(a, t, k1);
+    const int32_t mine_at = static_cast<int32_t>(lane % kKeys);   // the key whose page this lane looks up
 
-    // page of the block's key `lane % 32`, or -1.  Keys without a page are
-    // loaded from page 0: their scores are masked, their values get weight 0.
-    auto pages_at = [&](int32_t kb) -> int32_t {
-        const int32_t p = kb + static_cast<int32_t>(lane % kBlockKeys);
-        if (p < t.seen || p >= k1) return -1;
-        const int32_t page = page_of(a.cache, a.batch, t.s, p);
-        bad |= page < 0;
-        return page;
-    };
-    // Piece j of a lane: 8 elements of key u / kUnits, neighbouring lanes
-    // along the key, so that a row is read in one run.
-    Piece kreg[kPer], vreg[kPer];
+    // Keys without a page are loaded from page 0: their scores are masked,
+    // their values get weight 0.
+    u32x4 kreg[kPer], vreg[kPer];
     auto load = [&](int32_t kb, int32_t pages) {
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
             const int32_t page = __shfl(pages, key);
-            const uint64_t off =
-                slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
-            kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off));
-            vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off));
+            const uint64_t off = slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * 16;
+            kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off));
+            vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off));
         }
     };
 
-    const int32_t step = kFewWaves * kBlockKeys;
-    int32_t kb = k0 + static_cast<int32_t>(wave * kBlockKeys);
-    int32_t pages = -1, next_pages = -1;
+    const int32_t step = kFewWaves * kKeys;
+    int32_t kb = k0 + static_cast<int32_t>(wave * kKeys);
+    int32_t pages = -1, asked = -1;
     if (kb < k1) {
-        pages = pages_at(kb);
+        pages = table.answer(kb + mine_at, table.ask(kb + mine_at));
+        asked = table.ask(kb + step + mine_at);
         load(kb, pages);
-        if (kb + step < k1) next_pages = pages_at(kb + step);
     }
     for (; kb < k1; kb += step) {
         const bool more = kb + step < k1;
+        const int32_t here_pages = pages;
         const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
+        // every row sees every key of the block?
+        const bool whole = here == ~0ull && kb >= a.mask.first(t.p1) &&
+                           kb + static_cast<int32_t>(kKeys) <= a.mask.last(t.p0, t.seq.kv);
+        bool special = false;   // a weight of 0 does not keep Inf and NaN out of the product
+        if (!whole)
+#pragma unroll
+            for (uint32_t j = 0; j < kPer; ++j) {
+                special |= not_finite<kE5M2>(vreg[j]);
+                vreg[j] = finite_part<kE5M2>(vreg[j]);
+            }
         wave_lds_order();
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
-            *lds_as<u32x4>(keys + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
-            *lds_as<u32x4>(values + key * kFewRow<D> + col * 16) = expand(vreg[j]);
+            *lds_as<u32x4>(keys + key * F::kK + col * 16) = kreg[j];
+            *lds_as<u32x4>(values + key * F::kV + col * 16) = vreg[j];
         }
         wave_lds_order();
         if (more) {
-            load(kb + step, next_pages);
-            pages = next_pages;
-            next_pages = kb + 2 * step < k1 ? pages_at(kb + 2 * step) : -1;
+            pages = table.answer(kb + step + mine_at, asked);
+            asked = table.ask(kb + 2 * step + mine_at);
+            load(kb + step, pages);
         }
-        f32x4 s[NT][2];
+        f32x4 s[kSub];
 #pragma unroll
-        for (uint32_t kt = 0; kt < 2; ++kt) {
-#pragma unroll
-            for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (uint32_t kt = 0; kt < kSub; ++kt) {
+            s[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (uint32_t f = 0; f < kFrags; ++f) {
+                const LdsBytes p = keys + (16 * kt + c16) * F::kK + (32 * f + 8 * g) * F::kSize;
+                u32x4 x;
+                if constexpr (kE5M2) x = expand(*lds_as<u32x2>(p));
+                else x = *lds_as<u32x4>(p);
                 // past the row's end (D = 80) Q is 0, and K must be too: LDS holds anything there
-                u32x4 x = *lds_as<u32x4>(keys + (16 * kt + c16) * kKeyRow<D> + 64 * f + 16 * g);
                 if (32 * f + 32 > D && 32 * f + 8 * g >= D) x = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (uint32_t nt = 0; nt < NT; ++nt) s[nt][kt] = mfma16<kE5M2>(x, q[nt][f], s[nt][kt]);
+                s[kt] = mfma16<kE5M2>(x, q[f], s[kt]);
             }
         }
-
-        // every row sees every key of the block?
-        const bool whole = here == ~0ull && kb >= a.mask.first(t.p1) &&
-                           kb + static_cast<int32_t>(kBlockKeys) <= a.mask.last(t.p0, t.seq.kv);
-        const int32_t kb4 = kb + static_cast<int32_t>(4 * g);
-        const uint32_t mine = static_cast<uint32_t>(here >> (4 * g));
-        u32x4 p[NT];
+        if (!whole) {
+            const int32_t lo = first - kb - static_cast<int32_t>(4 * g), hi = last - kb - static_cast<int32_t>(4 * g);
+            const uint64_t mine = here >> (4 * g);
 #pragma unroll
-        for (uint32_t nt = 0; nt < NT; ++nt) {
-            if (!whole) {
+            for (uint32_t kt = 0; kt < kSub; ++kt)
 #pragma unroll
-                for (uint32_t kt = 0; kt < 2; ++kt)
+                for (uint32_t j = 0; j < 4; ++j) {
+                    const int32_t i = static_cast<int32_t>(16 * kt + j);   // key i + 4 g
+                    s[kt][j] = i >= lo && i < hi && (mine >> i & 1) ? s[kt][j] : -kInf;
+                }
+        }
+        float top = s[0][0];
 #pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) {
-                        // key 16 kt + 4 g + j
-                        const int32_t i = static_cast<int32_t>(16 * kt + j);
-                        const bool sees = i >= first[nt] - kb4 && i < last[nt] - kb4 && (mine >> i & 1);
-                        s[nt][kt][j] = sees ? s[nt][kt][j] : -kInf;
-                    }
-            }
-            float top = s[nt][0][0];
+        for (uint32_t i = 1; i < 4 * kSub; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+        top = row_max(top) * c;
+        if (__any(top > m + kSlack)) {
+            const float now = fmaxf(m, top), r = now == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            l *= r;
 #pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[nt][i / 4][i % 4]);
-            top = row_max(top) * c[nt];
-            const float was = m[nt], now = fmaxf(was, top);
-            const float base = now == -kInf ? 0.f : now;
-            if (__any(now > was)) {
-                const float r = __builtin_amdgcn_exp2f(was - base);
-                l[nt] *= r;
+            for (uint32_t d = 0; d < kTiles; ++d) o[d] *= r;
+        }
+        const float base = m == -kInf ? 0.f : m;
+        u32x4 p[kSub / 2];
 #pragma unroll
-                for (uint32_t d = 0; d < kTiles; ++d) o[nt][d] *= r;
-            }
-            m[nt] = now;
+        for (uint32_t kk = 0; kk < kSub / 2; ++kk) {
             f32x8 e;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][i / 4][i % 4], c[nt], -base));
-                l[nt] += e[i];
+            for (uint32_t i = 0; i < 8; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * kk + i / 4][i % 4], c, -base));
+                l += e[i];
             }
-            p[nt] = pack<kE5M2>(e);
+            p[kk] = pack<kE5M2>(e);
         }
-
-        const LdsBytes read = values + (4 * g + c16 / 4) * kFewRow<D> + c16 % 4 * 8;
-        auto value = [&](uint32_t d) {   // V^T operand of elements 16 d ..
-            const u32x2 lo = read_tr16(read + d * 32), hi = read_tr16(read + 16 * kFewRow<D> + d * 32);
-            return u32x4{lo[0], lo[1], hi[0], hi[1]};
-        };
-        bool special = false;
-        if (!whole)
 #pragma unroll
-            for (uint32_t d = 0; d < kTiles; ++d) special |= not_finite<kE5M2>(value(d));
-        if (!__any(special)) {
+        for (uint32_t kk = 0; kk < kSub / 2; ++kk)
 #pragma unroll
             for (uint32_t d = 0; d < kTiles; ++d) {
-                const u32x4 v = value(d);
-#pragma unroll
-                for (uint32_t nt = 0; nt < NT; ++nt) o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
+                // V^T operand: element 16 d + c16 of the keys 32 kk + 4 g .. + 3 and 32 kk + 16 + 4 g .. + 3
+                u32x4 v;
+                if constexpr (kE5M2) {   // 2 lanes a row
+                    const uint32_t r = c16 / 2, key = 32 * kk + 4 * g + r % 4 + r / 4 * 16;
+                    v = expand(read_tr8(values + key * F::kV + 16 * d + c16 % 2 * 8));
+                } else {                 // 4 lanes a row
+                    const LdsBytes row = values + (32 * kk + 4 * g + c16 / 4) * F::kV + 32 * d + c16 % 4 * 8;
+                    const u32x2 lo = read_tr16(row), hi = read_tr16(row + 16 * F::kV);
+                    v = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                }
+                o[d] = mfma16<kE5M2>(v, p[kk], o[d]);
             }
-        } else {
-            // a weight of 0 would not keep an Inf or NaN that a row does not see out of the product
-#pragma unroll
-            for (uint32_t d = 0; d < kTiles; ++d) {
-                const u32x4 v = finite_part<kE5M2>(value(d));
-#pragma unroll
-                for (uint32_t nt = 0; nt < NT; ++nt) o[nt][d] = mfma16<kE5M2>(v, p[nt], o[nt][d]);
-            }
+        if (__any(special)) {   // to the rows that see them
 #pragma unroll 1
-            for (uint32_t key = 0; key < kBlockKeys; ++key) {
-                const int32_t at = kb + static_cast<int32_t>(key);
+            for (uint32_t key = 0; key < kKeys; ++key) {
+                const int32_t pos = kb + static_cast<int32_t>(key), page = __builtin_amdgcn_readlane(here_pages, key);
+                if (page < 0 || pos < first || pos >= last) continue;
+                const SZ_GLOBAL uint8_t* row = pool_v + slot_offset(a.cache, page, pos);
 #pragma unroll
-                for (uint32_t nt = 0; nt < NT; ++nt) {
-                    if (at < first[nt] || at >= last[nt] || !(here >> key & 1)) continue;
-#pragma unroll
-                    for (uint32_t d = 0; d < kTiles; ++d) {
-                        float x[4] = {o[nt][d][0], o[nt][d][1], o[nt][d][2], o[nt][d][3]};
-                        add_not_finite<kE5M2>(*lds_as<u32x2>(values + key * kFewRow<D> + 32 * d + 8 * g), x);
-                        o[nt][d] = f32x4{x[0], x[1], x[2], x[3]};
-                    }
+                for (uint32_t d = 0; d < kTiles; ++d) {
+                    float x[4] = {o[d][0], o[d][1], o[d][2], o[d][3]};
+                    add_not_finite<kE5M2>(row + (16 * d + 4 * g) * F::kSize, x);
+                    o[d] = f32x4{x[0], x[1], x[2], x[3]};
                 }
             }
         }
     }
-    if (__any(bad) && lane == 0) flag(a.status);
+    if (__any(table.bad) && lane == 0) flag(a.status);
 
     // ---- join the 4 waves
-    f32x2* stats = reinterpret_cast<f32x2*>(lds + few_lds_bytes<D, NT>() - kFewWaves * M * 8);   // [wave][row]
+    KV_LDS f32x2* stats = lds_as<f32x2>((LdsBytes)lds + (F::kLds - kFewWaves * 16 * 8));   // [wave][row]
+    KV_LDS float* sums = lds_as<float>((LdsBytes)lds);                                   // [wave][row][D + 4]
+    l = row_sum(l);
+    __syncthreads();   // the stages have been read
+    if (g == 0) stats[wave * 16 + c16] = f32x2{m, l};
 #pragma unroll
-    for (uint32_t nt = 0; nt < NT; ++nt) {
-        const float sum = row_sum(l[nt]);
-        if (g == 0) stats[wave * M + 16 * nt + c16] = f32x2{m[nt], sum};
-    }
-    float* sums = reinterpret_cast<float*>(lds);   // [wave][16 rows][D + 4]
+    for (uint32_t d = 0; d < kTiles; ++d)
+        *(KV_LDS f32x4*)(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[d];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kFewThreads) {
+        const uint32_t row = i / (D / 4), d4 = i % (D / 4) * 4;
+        if (row >= t.rows) break;
+        float top = -kInf;
+        f32x2 st[kFewWaves];
 #pragma unroll
-    for (uint32_t nt = 0; nt < NT; ++nt) {
-        __syncthreads();   // the stages, or the last tile's sums, have been read
+        for (uint32_t w = 0; w < kFewWaves; ++w) {
+            st[w] = stats[w * 16 + row];
+            top = fmaxf(top, st[w][0]);
+        }
+        const float base = top == -kInf ? 0.f : top;
+        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        float sum = 0.f;
 #pragma unroll
-        for (uint32_t d = 0; d < kTiles; ++d)
-            *reinterpret_cast<f32x4*>(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[nt][d];
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kFewThreads) {
-            const uint32_t row = i / (D / 4), d4 = i % (D / 4) * 4;
-            if (16 * nt + row >= t.rows) continue;
-            float top = -kInf;
-            f32x2 st[kFewWaves];
+        for (uint32_t w = 0; w < kFewWaves; ++w) {
+            const float r = __builtin_amdgcn_exp2f(st[w][0] - base);
+            sum += r * st[w][1];
+            acc += r * *(KV_LDS f32x4*)(sums + (w * 16 + row) * (D + 4) + d4);
+        }
+        const RowAt to = row_at(t, t.row0 + row, a.group, kv_head);
+        if (splits <= 1) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            const float inv = 1.f / sum;
+            f32x4 y;
 #pragma unroll
-            for (uint32_t w = 0; w < kFewWaves; ++w) {
-                st[w] = stats[w * M + 16 * nt + row];
-                top = fmaxf(top, st[w][0]);
-            }
-            const float base = top == -kInf ? 0.f : top;
-            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-            float sum = 0.f;
-#pragma unroll
-            for (uint32_t w = 0; w < kFewWaves; ++w) {
-                const float r = __builtin_amdgcn_exp2f(st[w][0] - base);
-                sum += r * st[w][1];
-                acc += r * *reinterpret_cast<const f32x4*>(sums + (w * 16 + row) * (D + 4) + d4);
-            }
-            const RowAt at = row_at(t, t.row0 + 16 * nt + row, a.group, kv_head);
-            if (splits <= 1) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                f32x4 y;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] * inv;
-                *reinterpret_cast<SZ_GLOBAL u32x2*>(gptr(a.out) + static_cast<uint64_t>(at.token) * a.out_stride +
-                                                    at.head * D + d4) =
-                    __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
-                if (d4 == 0) put_lse(a, at, base, sum);
-            } else {
-                const uint64_t r = (static_cast<uint64_t>(at.token) * (a.group * a.cache.kv_heads) + at.head) * a.splits +
-                                   blockIdx.y;
-                *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
-                if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
-            }
+            for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] * inv;
+            *reinterpret_cast<SZ_GLOBAL u32x2*>(gptr(a.out) + static_cast<uint64_t>(to.token) * a.out_stride +
+                                                to.head * D + d4) =
+                __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
+            if (d4 == 0) put_lse(a, to, base, sum);
+        } else {
+            const uint64_t r =
+                (static_cast<uint64_t>(to.token) * (a.group * a.cache.kv_heads) + to.head) * a.splits + blockIdx.y;
+            *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
+            if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
         }
     }
 }
@@ -514,10 +541,12 @@ constexpr uint32_t kValueRow = ((2 * D + 63) / 64 | 1) * 64;      // V rows: 4 r
 
 template <uint32_t D, bool kE5M2, uint32_t N>
 __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(AttentionArgs a) {
-    constexpr uint32_t M = kTileRows, kFrags = D / 16, kTiles = (D + 31) / 32, kUnits = D / 8, kSub = N / 32;
+    constexpr uint32_t M = kTileRows, kFrags = D / 16, kTiles = (D + 31) / 32, kSub = N / 32;
+    constexpr uint32_t kSize = kE5M2 ? 1 : 2, kUnits = D * kSize / 16;   // 16-byte pieces of a row of the cache
     constexpr uint32_t kPieces = N * kUnits, kPer = (kPieces + kTileThreads - 1) / kTileThreads;
     constexpr uint32_t kBuffer = N * (kKeyRow<D> + kValueRow<D>);
     __shared__ __align__(16) uint8_t lds[2 * kBuffer];
+    __shared__ int32_t marks[2];   // first key of the tile in each buffer, if Inf or NaN were left out of it
     const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
     const uint64_t slot = blockIdx.x / a.cache.kv_heads;
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
@@ -551,25 +580,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     for (uint32_t f = 0; f < kFrags; ++f)
         q[f] = live ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 16 * f + 8 * half) : u32x4{0, 0, 0, 0};
     float c = a.scale * kLog2e;
-    if constexpr (kE5M2) {
-        float most = 0.f;
-#pragma unroll
-        for (uint32_t f = 0; f < kFrags; ++f) {
-            const f32x8 x = to_f32(q[f]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
-        }
-        most = fmaxf(swap32(most, false), swap32(most, true));
-        const int32_t up = most > 0.f && most < kInf ? 15 - __builtin_amdgcn_frexp_expf(most) : 0;
-#pragma unroll
-        for (uint32_t f = 0; f < kFrags; ++f) {
-            f32x8 x = to_f32(q[f]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_ldexpf(x[j], up);
-            q[f] = pack<true>(x);
-        }
-        c = __builtin_amdgcn_ldexpf(c, -up);
-    }
+    if constexpr (kE5M2) c = to_fp16<kFrags>(q, c, [](float x) { return fmaxf(swap32(x, false), swap32(x, true)); });
     c = fmaxf(c, 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
 
     f32x16 o[kTiles];
@@ -581,69 +592,100 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
 
     const SZ_GLOBAL uint8_t* pool_k = gptr(a.cache.k) + kv_head * a.cache.head_stride;
     const SZ_GLOBAL uint8_t* pool_v = gptr(a.cache.v) + kv_head * a.cache.head_stride;
-    bool bad = false;
-    auto pages_at = [&](int32_t kb) -> int32_t {   // page of the tile's key `lane % N`, or -1
-        const int32_t p = kb + static_cast<int32_t>(lane % N);
-        if (p < t.seen || p >= k1) return -1;
-        const int32_t page = page_of(a.cache, a.batch, t.s, p);
-        bad |= page < 0;
-        return page;
-    };
-    typedef typename std::conditional<kE5M2, u32x2, u32x4>::type Piece;
-    Piece kreg[kPer], vreg[kPer];
-    auto load = [&](int32_t kb, int32_t pages) {
+    Pages table(a, t, k1);
+    const int32_t mine_at = static_cast<int32_t>(lane % N);   // the key whose page this lane looks up
+    u32x4 kreg[kPer], vreg[kPer];
+    uint64_t off[kPer];   // where the thread's pieces of the tile are; keys without a page are loaded from page 0
+    auto find = [&](int32_t kb, int32_t pages) {
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits % N, col = u % kUnits;
             const int32_t page = __shfl(pages, key);
-            const uint64_t off =
-                slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * sizeof(Piece);
-            kreg[j] = *reinterpret_cast<const SZ_GLOBAL Piece*>(pool_k + off);
-            vreg[j] = *reinterpret_cast<const SZ_GLOBAL Piece*>(pool_v + off);
+            off[j] = slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * 16;
         }
     };
-    auto put = [&](LdsBytes buffer) {
+    auto load = [&](u32x4* to, const SZ_GLOBAL uint8_t* pool) {
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) to[j] = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool + off[j]);
+    };
+    // Rows of the tile all see all of [all_from, all_to); a tile of keys that
+    // is not inside, or has keys without a page, is an edge.
+    const int32_t tile_from = a.mask.first(t.p1), tile_to = a.mask.last(t.p0, t.seq.kv);
+    auto is_edge = [&](int32_t kb, uint64_t here) {
+        return here != ~0ull || kb < tile_from || kb + static_cast<int32_t>(N) > tile_to;
+    };
+    // The pieces into LDS, as 16-bit values.  On an edge a weight of 0 would
+    // not keep an Inf or NaN out of the product: they are left out, and the
+    // buffer's mark says so.
+    auto put = [&](uint32_t turn, int32_t kb, bool edge) {
+        const LdsBytes buffer = (LdsBytes)lds + turn * kBuffer;
+        if (edge) {
+            bool special = false;
+#pragma unroll
+            for (uint32_t j = 0; j < kPer; ++j) {
+                special |= not_finite<kE5M2>(vreg[j]);
+                vreg[j] = finite_part<kE5M2>(vreg[j]);
+            }
+            if (special) marks[turn] = kb;
+        }
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
             const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits, col = u % kUnits;
             if (kPieces % kTileThreads && u >= kPieces) break;
-            *lds_as<u32x4>(buffer + key * kKeyRow<D> + col * 16) = expand(kreg[j]);
-            *lds_as<u32x4>(buffer + N * kKeyRow<D> + key * kValueRow<D> + col * 16) = expand(vreg[j]);
+            const LdsBytes k = buffer + key * kKeyRow<D>, v = buffer + N * kKeyRow<D> + key * kValueRow<D>;
+            if constexpr (kE5M2) {
+                *lds_as<u32x4>(k + col * 32) = expand(u32x2{kreg[j][0], kreg[j][1]});
+                *lds_as<u32x4>(k + col * 32 + 16) = expand(u32x2{kreg[j][2], kreg[j][3]});
+                *lds_as<u32x4>(v + col * 32) = expand(u32x2{vreg[j][0], vreg[j][1]});
+                *lds_as<u32x4>(v + col * 32 + 16) = expand(u32x2{vreg[j][2], vreg[j][3]});
+            } else {
+                *lds_as<u32x4>(k + col * 16) = kreg[j];
+                *lds_as<u32x4>(v + col * 16) = vreg[j];
+            }
         }
     };
 
-    int32_t pages = k0 < k1 ? pages_at(k0) : -1, next = -1;
+    constexpr int32_t kStep = static_cast<int32_t>(N);
+    int32_t pages = -1, asked = -1;
     if (k0 < k1) {
-        load(k0, pages);
-        next = pages_at(k0 + static_cast<int32_t>(N));
-        put((LdsBytes)lds);
+        pages = table.answer(k0 + mine_at, table.ask(k0 + mine_at));
+        asked = table.ask(k0 + kStep + mine_at);
+        find(k0, pages);
+        load(kreg, pool_k);
+        load(vreg, pool_v);
+        if (threadIdx.x < 2) marks[threadIdx.x] = -1;
+        __syncthreads();
+        put(0, k0, is_edge(k0, __ballot(pages >= 0)));
     }
     uint32_t turn = 0;
-    for (int32_t kb = k0; kb < k1; kb += static_cast<int32_t>(N), turn ^= 1) {
-        const bool more = kb + static_cast<int32_t>(N) < k1;
+    for (int32_t kb = k0; kb < k1; kb += kStep, turn ^= 1) {
+        const bool more = kb + kStep < k1;
+        const int32_t here_pages = pages;
         const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
         const LdsBytes buffer = (LdsBytes)lds + turn * kBuffer;
-        auto fetch = [&] {
-            if (!more) return;
-            load(kb + static_cast<int32_t>(N), next);
-            pages = next;
-            next = pages_at(kb + 2 * static_cast<int32_t>(N));
-        };
         __syncthreads();   // this tile is in LDS; the other buffer has been read by every wave
-        if (kb < any_to && kb + static_cast<int32_t>(N) > any_from) {
+        if (more) {
+            pages = table.answer(kb + kStep + mine_at, asked);
+            asked = table.ask(kb + 2 * kStep + mine_at);
+            find(kb + kStep, pages);
+            load(kreg, pool_k);
+        }
+        if (kb < any_to && kb + kStep > any_from) {
             f32x16 s[kSub];
 #pragma unroll
-            for (uint32_t kt = 0; kt < kSub; ++kt) {
+            for (uint32_t kt = 0; kt < kSub; ++kt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-                for (uint32_t f = 0; f < kFrags; ++f) {
+            for (uint32_t f = 0; f < kFrags; ++f)
+#pragma unroll
+                for (uint32_t kt = 0; kt < kSub; ++kt) {
                     const u32x4 x = *lds_as<u32x4>(buffer + (32 * kt + c32) * kKeyRow<D> + 32 * f + 16 * half);
                     s[kt] = mfma32<kE5M2>(x, q[f], s[kt]);
                 }
-            }
-            fetch();   // behind the first product: its registers are then free
-            const bool whole = here == ~0ull && kb >= all_from && kb + static_cast<int32_t>(N) <= all_to;
+            interleave<kFrags * kSub, 1, 4>();
+            if (more) load(vreg, pool_v);
+            const bool whole = here == ~0ull && kb >= all_from && kb + kStep <= all_to;
             if (!whole) {
                 const int32_t from = first - kb - static_cast<int32_t>(4 * half), to = last - kb - static_cast<int32_t>(4 * half);
 #pragma unroll
@@ -662,75 +704,62 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
 #pragma unroll
             for (uint32_t i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
             top = fmaxf(swap32(top, false), swap32(top, true)) * c;
-            const float was = m, now = fmaxf(was, top);
-            const float base = now == -kInf ? 0.f : now;
-            if (__any(now > was)) {
-                const float r = __builtin_amdgcn_exp2f(was - base);
+            if (__any(top > m + kSlack)) {
+                const float now = fmaxf(m, top), r = now == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - now);
+                m = now;
                 l *= r;
 #pragma unroll
                 for (uint32_t d = 0; d < kTiles; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= r;
             }
-            m = now;
-            u32x4 p[2 * kSub];
-#pragma unroll
-            for (uint32_t kk = 0; kk < 2 * kSub; ++kk) {
+            const float base = m == -kInf ? 0.f : m;
+            auto weights = [&](uint32_t kk) {   // P^T operand of keys 16 kk ..
                 f32x8 e;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kk / 2][8 * (kk % 2) + i], c, -base));
                     l += e[i];
                 }
-                p[kk] = pack<kE5M2>(e);
-            }
+                return pack<kE5M2>(e);
+            };
             const LdsBytes values = buffer + N * kKeyRow<D>;
             const LdsBytes read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
-            auto value = [&](uint32_t kk, uint32_t d) {   // V^T operand of keys 16 kk .., elements 32 d ..
-                const u32x2 lo = read_tr16(read + 16 * kk * kValueRow<D> + 64 * d);
-                const u32x2 hi = read_tr16(read + (16 * kk + 8) * kValueRow<D> + 64 * d);
-                return u32x4{lo[0], lo[1], hi[0], hi[1]};
-            };
-            bool special = false;
-            if (!whole)
 #pragma unroll
-                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
+            for (uint32_t kk = 0; kk < 2 * kSub; ++kk) {
+                const u32x4 p = weights(kk);
 #pragma unroll
-                    for (uint32_t d = 0; d < kTiles; ++d) special |= not_finite<kE5M2>(value(kk, d));
-            if (!__any(special)) {
-#pragma unroll
-                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
-#pragma unroll
-                    for (uint32_t d = 0; d < kTiles; ++d) o[d] = mfma32<kE5M2>(value(kk, d), p[kk], o[d]);
-            } else {
-                // a weight of 0 would not keep an Inf or NaN that a row does not see out of the product
-#pragma unroll
-                for (uint32_t kk = 0; kk < 2 * kSub; ++kk)
-#pragma unroll
-                    for (uint32_t d = 0; d < kTiles; ++d)
-                        o[d] = mfma32<kE5M2>(finite_part<kE5M2>(value(kk, d)), p[kk], o[d]);
+                for (uint32_t d = 0; d < kTiles; ++d) {
+                    const u32x2 lo = read_tr16(read + 16 * kk * kValueRow<D> + 64 * d);
+                    const u32x2 hi = read_tr16(read + (16 * kk + 8) * kValueRow<D> + 64 * d);
+                    o[d] = mfma32<kE5M2>(u32x4{lo[0], lo[1], hi[0], hi[1]}, p, o[d]);
+                }
+            }
+            interleave<2 * kSub * kTiles, 2, 4>();
+            if (is_edge(kb, here) && marks[turn] == kb) {   // Inf and NaN, to the rows that see them
 #pragma unroll 1
                 for (uint32_t key = 0; key < N; ++key) {
-                    const int32_t p = kb + static_cast<int32_t>(key);
-                    if (p < first || p >= last || !(here >> key & 1)) continue;
+                    const int32_t p = kb + static_cast<int32_t>(key), page = __builtin_amdgcn_readlane(here_pages, key);
+                    if (page < 0 || p < first || p >= last) continue;
+                    const SZ_GLOBAL uint8_t* from_v = pool_v + slot_offset(a.cache, page, p);
 #pragma unroll
                     for (uint32_t d = 0; d < kTiles; ++d)
 #pragma unroll
                         for (uint32_t b = 0; b < 4; ++b) {
+                            if (32 * d + 8 * b >= D) continue;
                             float x[4] = {o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
-                            add_not_finite<kE5M2>(
-                                *lds_as<u32x2>(values + key * kValueRow<D> + 64 * d + 16 * b + 8 * half), x);
+                            add_not_finite<kE5M2>(from_v + (32 * d + 8 * b + 4 * half) * kSize, x);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) o[d][4 * b + i] = x[i];
                         }
                 }
             }
-        } else {
-            fetch();
+        } else if (more) {
+            load(vreg, pool_v);
         }
-        if (more) put((LdsBytes)lds + (turn ^ 1) * kBuffer);
+        if (more) put(turn ^ 1, kb + kStep, is_edge(kb + kStep, __ballot(pages >= 0)));
     }
-    if (__any(bad) && lane == 0) flag(a.status);
+    if (__any(table.bad) && lane == 0) flag(a.status);
 
     const float sum = swap32(l, false) + swap32(l, true);
     const float base = m == -kInf ? 0.f : m;
@@ -824,8 +853,7 @@ template <uint32_t D, bool kE5M2>
 hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
     const dim3 grid(static_cast<uint32_t>(slots * a.cache.kv_heads), a.splits);
-    if (a.tile == 16) k_attend_few<D, kE5M2, 1><<<grid, kFewThreads, 0, s>>>(a);
-    else if (a.tile == 32) k_attend_few<D, kE5M2, 2><<<grid, kFewThreads, 0, s>>>(a);
+    if (a.tile == 16) k_attend_few<D, kE5M2><<<grid, kFewThreads, 0, s>>>(a);
     else k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
     if (a.splits > 1) {
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
