@@ -239,7 +239,10 @@ kvi::AttentionPlan kvi::attention_plan(uint32_t kv_heads, uint32_t group, uint32
     if (window && static_cast<uint64_t>(window) + p.tile + 32 < range) range = static_cast<uint64_t>(window) + p.tile + 32;
     if (range == 0) range = 1;
     const uint64_t rows = static_cast<uint64_t>(total_tokens) * group;
-    const uint64_t tiles = (rows / p.tile + (rows / p.tile < num_seqs ? rows / p.tile : num_seqs) + 1) * kv_heads;
+    uint64_t tiles = rows / p.tile + num_seqs;
+    const uint64_t each = (most_rows + p.tile - 1) / p.tile;
+    if (num_seqs * each < tiles) tiles = num_seqs * each;
+    tiles *= kv_heads;
     // Enough workgroups to fill the GPU, each with at least 256 positions.
     const uint64_t kGroups = p.tile == 128 ? 512 : 1024, kLeast = 256;
     uint64_t splits = tiles < kGroups ? (kGroups + tiles - 1) / tiles : 1;

@@ -798,15 +798,19 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     }
 }
 
-// Joins the splits of each row: one wave a row, D / 64 (or fewer lanes) sums a lane.
+// Joins the splits of each row, a row a workgroup: D / 4 lanes a split, so
+// that 3 (D = 256: 4) to 16 splits are read at a time, and a sum over them
+// through LDS.
+constexpr uint32_t kJoinThreads = 256;
+
 template <uint32_t D>
-__global__ __launch_bounds__(256) void k_join(AttentionArgs a) {
+__global__ __launch_bounds__(kJoinThreads) void k_join(AttentionArgs a) {
+    constexpr uint32_t kLanes = D / 4, kSets = kJoinThreads / kLanes;
+    __shared__ f32x4 sums[kSets * kLanes];
+    __shared__ float wave_top[kJoinThreads / 64], weights[kSets];
     const uint32_t heads = a.group * a.cache.kv_heads;
-    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
-    const uint32_t lane = threadIdx.x % 64;
-    if (row >= static_cast<uint64_t>(a.batch.total_tokens) * heads) return;
-    const uint32_t token = uniform(static_cast<uint32_t>(row / heads)), head = static_cast<uint32_t>(row % heads);
-    const uint32_t s = seq_of_token(a.batch, token);
+    const uint32_t row = blockIdx.x, token = row / heads, head = row - token * heads;
+    const uint32_t s = uniform(seq_of_token(a.batch, token));
     if (s >= a.batch.num_seqs) return;
     Tile t{};
     t.seq = span_of(a.batch, s);
@@ -817,36 +821,53 @@ __global__ __launch_bounds__(256) void k_join(AttentionArgs a) {
     const uint32_t rows = static_cast<uint32_t>(t.seq.n) * a.group - t.row0;
     t.rows = rows < a.tile ? rows : a.tile;
     tile_range(t, a.mask, a.group);
-    const uint32_t splits = splits_of(t, a.split_len);
+    const uint32_t splits = uniform(splits_of(t, a.split_len));
     if (splits <= 1) return;   // written by its workgroup
-    const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a))) + row * a.splits;
+
+    const uint64_t first = static_cast<uint64_t>(row) * a.splits;
+    const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a))) + first;
     float top = -kInf;
-    for (uint32_t z = 0; z < splits; ++z)
+    for (uint32_t z = threadIdx.x; z < splits; z += kJoinThreads)
         if (stats[z][1] != 0.f) top = fmaxf(top, stats[z][0]);
+    for (uint32_t m = 32; m; m /= 2) top = fmaxf(top, __shfl_xor(top, m));
+    if (threadIdx.x % 64 == 0) wave_top[threadIdx.x / 64] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
     const float base = top == -kInf ? 0.f : top;
-    const SZ_GLOBAL float* part = gptr(a.part) + row * a.splits * D;
-    constexpr uint32_t kPer = (D + 63) / 64;
-    float acc[kPer] = {};
-    float sum = 0.f;
-    for (uint32_t z = 0; z < splits; ++z) {
-        const f32x2 st = stats[z];
-        if (st[1] == 0.f) continue;
-        const float r = __builtin_amdgcn_exp2f(st[0] - base);
-        sum += r * st[1];
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; ++i) {
-            const uint32_t d = lane + 64 * i;
-            if (d < D) acc[i] += r * part[z * D + d];
+
+    const uint32_t set = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    if (set < kSets) {
+        const SZ_GLOBAL f32x4* part = reinterpret_cast<const SZ_GLOBAL f32x4*>(gptr(a.part) + first * D) + lane;
+        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        float sum = 0.f;
+#pragma unroll 4
+        for (uint32_t z = set; z < splits; z += kSets) {
+            const f32x2 st = stats[z];
+            const f32x4 x = part[z * kLanes];
+            if (st[1] != 0.f) {   // a split whose keys the row does not see has no maximum
+                const float r = __builtin_amdgcn_exp2f(st[0] - base);
+                sum += r * st[1];
+                acc += r * x;
+            }
         }
+        sums[set * kLanes + lane] = acc;
+        if (lane == 0) weights[set] = sum;
     }
+    __syncthreads();
+    if (threadIdx.x >= kLanes) return;
+    f32x4 acc = sums[threadIdx.x];
+    float sum = weights[0];
+    for (uint32_t i = 1; i < kSets; ++i) {
+        acc += sums[i * kLanes + threadIdx.x];
+        sum += weights[i];
+    }
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    f32x4 y;
 #pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i) {
-        const uint32_t d = lane + 64 * i;
-        if (d >= D) continue;
-        const __bf16 y = static_cast<__bf16>(sum == 0.f ? 0.f : acc[i] / sum);
-        gptr(a.out)[static_cast<uint64_t>(token) * a.out_stride + head * D + d] = __builtin_bit_cast(uint16_t, y);
-    }
-    if (lane == 0) put_lse(a, RowAt{token, head, 0}, base, sum);
+    for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] / sum;
+    *reinterpret_cast<SZ_GLOBAL u32x2*>(gptr(a.out) + static_cast<uint64_t>(token) * a.out_stride + head * D +
+                                        threadIdx.x * 4) = __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
+    if (threadIdx.x == 0) put_lse(a, RowAt{token, head, 0}, base, sum);
 }
 
 template <uint32_t D, bool kE5M2>
@@ -857,7 +878,7 @@ hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     else k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
     if (a.splits > 1) {
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
-        k_join<D><<<static_cast<uint32_t>((rows + 3) / 4), 256, 0, s>>>(a);
+        k_join<D><<<static_cast<uint32_t>(rows), kJoinThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

@@ -38,7 +38,7 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t) {
     EXPECT(a.splits >= 1 && a.splits <= 65535 && a.split_len % 32 == 0);
     EXPECT(uint64_t(a.splits) * a.split_len >= (a.mask.window ? 1 : a.batch.max_kv_len));
     if (a.splits > 1) EXPECT(a.part && g_workspace >= rows * a.splits * (a.cache.head_dim + 2) * 4);
-    if (a.splits > 1) EXPECT((rows + 3) / 4 < (1u << 24));
+    if (a.splits > 1) EXPECT(rows < (1u << 24));
     return hipSuccess;
 }
 }  // namespace kvi
