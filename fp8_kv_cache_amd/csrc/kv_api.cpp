@@ -104,7 +104,10 @@ bool take_attention(const kv_cache* cache, const kv_batch* batch, const kv_atten
         return false;
     const AttentionPlan plan = attention_plan(a.cache.kv_heads, a.group, a.cache.head_dim, a.batch.num_seqs,
                                               a.batch.total_tokens, a.batch.max_tokens, a.batch.max_kv_len, x->window);
-    if (tile_slots(a.batch, a.group, plan.tile) * a.cache.kv_heads >= kMaxGroups) return false;
+    const uint64_t slots = tile_slots(a.batch, a.group, plan.tile);
+    if (plan.tile == 16 ? few_groups(slots, plan.splits, a.cache.kv_heads) >= kMaxGroups
+                        : slots * a.cache.kv_heads >= kMaxGroups)
+        return false;
     a.tile = plan.tile;
     a.splits = plan.splits;
     a.split_len = plan.split_len;

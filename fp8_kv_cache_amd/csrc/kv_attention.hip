@@ -21,27 +21,12 @@
 // two that brings its largest element to [2^14, 2^15) before it becomes FP16
 // (and c by its inverse): elements down to 2^-28 of the largest keep all of
 // BF16's bits, smaller ones lose less than 2^-38 of the largest.
-#include "kv_internal.h"
-
-#include <type_traits>
-
-#include "device_common.h"
-#include "splitzip.h"
+#include "kv_device.h"
 
 namespace kvi {
 
 namespace {
 
-using sz::gptr;
-using sz::u32x2;
-using sz::u32x4;
-using sz::uniform;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -67,12 +52,6 @@ __device__ inline u32x2 read_tr8(LdsBytes p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(lds_as<i32x2>(p)));
 }
 
-__device__ inline void flag(int32_t* status) {
-    if (status) *gptr(status) = SZ_ERR_INVALID_ARGUMENT;
-}
-
-__device__ inline f32x8 to_f32(u32x4 x) { return __builtin_convertvector(__builtin_bit_cast(bf16x8, x), f32x8); }
-
 // 8 E5M2 bytes -> 8 FP16
 __device__ inline u32x4 expand(u32x2 b) {
     return u32x4{sz::perm(0, b[0], 0x010C000Cu), sz::perm(0, b[0], 0x030C020Cu), sz::perm(0, b[1], 0x010C000Cu),
@@ -92,8 +71,6 @@ __device__ inline u32x4 pack(f32x8 x) {   // to the matrix cores' 16-bit type, n
     if constexpr (kE5M2) return __builtin_bit_cast(u32x4, __builtin_convertvector(x, f16x8));
     else return __builtin_bit_cast(u32x4, __builtin_convertvector(x, bf16x8));
 }
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <bool kE5M2>
 __device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
@@ -181,7 +158,7 @@ __device__ inline void wave_lds_order() {
 
 // The tile of a workgroup, its fields in scalar registers.
 __device__ inline Tile my_tile(const AttentionArgs& a, uint64_t slot, uint32_t M) {
-    Tile t = tile_of(a.batch, a.mask, slot, a.group, M);
+    Tile t = wave_tile_of(a.batch, a.mask, slot, a.group, M);
     auto scalar = [](int32_t& x) { x = __builtin_amdgcn_readfirstlane(x); };
     scalar(t.seq.begin);
     scalar(t.seq.n);
@@ -296,6 +273,10 @@ template <uint32_t D, bool kE5M2>
 struct Few {
     static constexpr uint32_t kKeys = kE5M2 ? 64 : 32;   // a block: 16 KB of K and V either way at D = 128
     static constexpr uint32_t kSize = kE5M2 ? 1 : 2;
+    // Rows of whole 128-byte lines are read once and kept in no cache (64 x 1
+    // to 8192 keys: 255 us, against 277 with plain loads); neighbouring heads
+    // share the lines of others (D = 80, 32 x 5 tokens: 115 us plain, 129).
+    static constexpr bool kOwnLines = D * kSize % 128 == 0;
     // rows in LDS; BF16 V: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
     static constexpr uint32_t kK = D * kSize + 16, kV = kE5M2 ? D + 16 : 2 * D + (D % 32 ? 0 : 32);
     static constexpr uint32_t kStage = kKeys * (kK + kV);
@@ -310,16 +291,23 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
     constexpr uint32_t kUnits = D * F::kSize / 16;   // 16-byte pieces of a row
     constexpr uint32_t kPer = kKeys * kUnits / 64;   // pieces of K, and of V, a lane has of a block
     __shared__ __align__(16) uint8_t lds[F::kLds];
-    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
-    const uint64_t slot = blockIdx.x / a.cache.kv_heads;
-    if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
-        !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
+    // Workgroups go to the 8 XCDs in turn.  The heads of a tile and split go
+    // to one of them, one after the other: in a token-major page their rows
+    // are neighbours, and lines that two rows share are read into one L2.
+    // The next split of a tile goes to the XCD before, so that sequences of
+    // different lengths load them alike.
+    const uint32_t turn = blockIdx.x / 8, kv_head = turn % a.cache.kv_heads;
+    const uint32_t unit = turn / a.cache.kv_heads * 8 + blockIdx.x % 8;
+    const uint32_t slots = static_cast<uint32_t>(tile_slots(a.batch, a.group, 16)), slots8 = (slots + 7) / 8 * 8;
+    const uint32_t split = unit / slots8, slot = (unit + split) % slots8;
+    if (slot >= slots) return;
+    if (kv_head == 0 && split == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 && !span_of(a.batch, slot).ok)
         flag(a.status);
     const Tile t = my_tile(a, slot, 16);
     if (!t.any) return;
     const uint32_t splits = splits_of(t, a.split_len);
-    if (blockIdx.y && blockIdx.y >= splits) return;
-    const int32_t k0 = t.lo + static_cast<int32_t>(blockIdx.y * a.split_len);
+    if (split && split >= splits) return;
+    const int32_t k0 = t.lo + static_cast<int32_t>(split * a.split_len);
     const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.split_len) ? t.hi : k0 + static_cast<int32_t>(a.split_len);
 
     const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16, c16 = lane % 16;
@@ -359,8 +347,10 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
             const uint32_t u = lane + 64 * j, key = u / kUnits, col = u % kUnits;
             const int32_t page = __shfl(pages, key);
             const uint64_t off = slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * 16;
-            kreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off));
-            vreg[j] = __builtin_nontemporal_load(reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off));
+            const SZ_GLOBAL u32x4* k = reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off);
+            const SZ_GLOBAL u32x4* v = reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off);
+            kreg[j] = F::kOwnLines ? __builtin_nontemporal_load(k) : *k;
+            vreg[j] = F::kOwnLines ? __builtin_nontemporal_load(v) : *v;
         }
     };
 
@@ -512,7 +502,6 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
         }
         const RowAt to = row_at(t, t.row0 + row, a.group, kv_head);
         if (splits <= 1) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
             const float inv = 1.f / sum;
             f32x4 y;
 #pragma unroll
@@ -523,7 +512,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
             if (d4 == 0) put_lse(a, to, base, sum);
         } else {
             const uint64_t r =
-                (static_cast<uint64_t>(to.token) * (a.group * a.cache.kv_heads) + to.head) * a.splits + blockIdx.y;
+                (static_cast<uint64_t>(to.token) * (a.group * a.cache.kv_heads) + to.head) * a.splits + split;
             *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
             if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
         }
@@ -810,11 +799,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttentionArgs a) {
     __shared__ float wave_top[kJoinThreads / 64], weights[kSets];
     const uint32_t heads = a.group * a.cache.kv_heads;
     const uint32_t row = blockIdx.x, token = row / heads, head = row - token * heads;
-    const uint32_t s = uniform(seq_of_token(a.batch, token));
-    if (s >= a.batch.num_seqs) return;
     Tile t{};
-    t.seq = span_of(a.batch, s);
-    if (!t.seq.ok || static_cast<int32_t>(token) < t.seq.begin) return;
+    t.seq = span_of(a.batch, wave_seq_of_token(a.batch, token));
+    if (static_cast<int32_t>(token) < t.seq.begin || static_cast<int32_t>(token) >= t.seq.begin + t.seq.n) return;
     // the tile that had the row
     const uint32_t at = (token - t.seq.begin) * a.group + head % a.group;
     t.row0 = at / a.tile * a.tile;
@@ -861,7 +848,6 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttentionArgs a) {
         acc += sums[i * kLanes + threadIdx.x];
         sum += weights[i];
     }
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     f32x4 y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] / sum;
@@ -872,10 +858,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttentionArgs a) {
 
 template <uint32_t D, bool kE5M2>
 hipError_t attend(const AttentionArgs& a, hipStream_t s) {
-    const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
-    const dim3 grid(static_cast<uint32_t>(slots * a.cache.kv_heads), a.splits);
-    if (a.tile == 16) k_attend_few<D, kE5M2><<<grid, kFewThreads, 0, s>>>(a);
-    else k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
+    const uint32_t slots = static_cast<uint32_t>(tile_slots(a.batch, a.group, a.tile));
+    if (a.tile == 16) {
+        k_attend_few<D, kE5M2><<<few_groups(slots, a.splits, a.cache.kv_heads), kFewThreads, 0, s>>>(a);
+    } else {
+        const dim3 grid(slots * a.cache.kv_heads, a.splits);
+        k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
+    }
     if (a.splits > 1) {
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
         k_join<D><<<static_cast<uint32_t>(rows), kJoinThreads, 0, s>>>(a);

@@ -114,18 +114,13 @@ KV_HD void tile_range(Tile& t, const Mask& mask, uint32_t group) {
     t.hi = mask.last(t.p1, t.seq.kv);
 }
 
-// The tile in `slot`; any = false where the slot has none.
-KV_HD Tile tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t group, uint32_t M) {
+// The tile in `slot` of sequence s, the last whose tile_slot is not above it;
+// any = false where there is none.
+KV_HD Tile tile_in(const Batch& b, const Mask& mask, uint32_t s, uint64_t slot, uint32_t group, uint32_t M) {
     Tile t{};
-    uint32_t lo = 0, hi = b.num_seqs;   // the last s with tile_slot(s) <= slot
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (tile_slot(b, mid, group, M) <= slot) lo = mid;
-        else hi = mid;
-    }
-    t.s = lo;
-    t.seq = span_of(b, lo);
-    const uint64_t first = tile_slot(b, lo, group, M);
+    t.s = s;
+    t.seq = span_of(b, s);
+    const uint64_t first = tile_slot(b, s, group, M);
     if (slot < first || !t.seq.ok) return t;
     const uint64_t row0 = (slot - first) * M, rows = static_cast<uint64_t>(t.seq.n) * group;
     if (row0 >= rows) return t;
@@ -136,9 +131,25 @@ KV_HD Tile tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t gro
     return t;
 }
 
+KV_HD Tile tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t group, uint32_t M) {
+    uint32_t lo = 0, hi = b.num_seqs;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (tile_slot(b, mid, group, M) <= slot) lo = mid;
+        else hi = mid;
+    }
+    return tile_in(b, mask, lo, slot, group, M);
+}
+
 // Splits of a tile's positions: split z has [lo + z * len, lo + (z + 1) * len) of [lo, hi).
 KV_HD uint32_t splits_of(const Tile& t, uint32_t len) {
     return t.hi > t.lo ? (static_cast<uint32_t>(t.hi - t.lo) + len - 1) / len : 0;
+}
+
+// Workgroups of the few-rows kernel: 8 tiles and splits at a time, each
+// with all KV heads.
+KV_HD uint64_t few_groups(uint64_t slots, uint64_t splits, uint64_t kv_heads) {
+    return (slots + 7) / 8 * 8 * splits * kv_heads;
 }
 
 // ---- launch interfaces

@@ -2,28 +2,13 @@
 // rotation, conversion and paged store in one pass) and the gather and
 // scatter between pages and contiguous layer tensors.  The calls are
 // documented in include/paged_kv.h.
-#include "kv_internal.h"
-
-#include "device_common.h"
-#include "splitzip.h"
+#include "kv_device.h"
 
 namespace kvi {
 
 namespace {
 
-using sz::gptr;
-using sz::u32x2;
-using sz::u32x4;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 constexpr uint32_t kThreads = 256;
-
-__device__ inline void flag(int32_t* status) {
-    if (status) *gptr(status) = SZ_ERR_INVALID_ARGUMENT;
-}
 
 // The place of token row t, the same for every thread of the workgroup:
 // false where nothing is to be done for it.
@@ -34,10 +19,9 @@ struct Place {
 __device__ inline bool place_of(const Cache& c, const Batch& b, uint32_t t, int32_t* status, Place& at) {
     for (uint32_t s = t; s < b.num_seqs; s += b.total_tokens)   // each sequence is looked at by one workgroup
         if (!span_of(b, s).ok && threadIdx.x == 0) flag(status);
-    at.s = seq_of_token(b, t);
-    if (at.s >= b.num_seqs) return false;
+    at.s = wave_seq_of_token(b, t);
     const Span seq = span_of(b, at.s);
-    if (!seq.ok || static_cast<int32_t>(t) < seq.begin) return false;
+    if (static_cast<int32_t>(t) < seq.begin || static_cast<int32_t>(t) >= seq.begin + seq.n) return false;
     at.p = seq.first() + (static_cast<int32_t>(t) - seq.begin);
     if (at.p < 0) {
         at.page = -1;
@@ -47,8 +31,6 @@ __device__ inline bool place_of(const Cache& c, const Batch& b, uint32_t t, int3
     if (at.page < 0 && threadIdx.x == 0) flag(status);
     return true;
 }
-
-__device__ inline f32x8 to_f32(u32x4 x) { return __builtin_convertvector(__builtin_bit_cast(bf16x8, x), f32x8); }
 
 // to E5M2, nearest even: byte i of the result is element i
 __device__ inline u32x2 to_e5m2(f32x8 x) {

@@ -55,6 +55,7 @@ class PagedCache:
         self.k, self.v, self.device = k, v, k.device
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.dtype = _CACHE_DTYPES[k.dtype]
+        self.dtypes = tuple(t for t, d in _CACHE_DTYPES.items() if d == self.dtype)   # of its layer tensors
         # a dimension of one entry may have any stride in torch; the library looks at no offset through it
         page, token, head = (s if n > 1 else 0 for n, s in zip(k.shape[:3], strides))
         self.raw = KvCache(k.data_ptr(), v.data_ptr(), page, token, head, self.num_pages, self.page_size,
@@ -120,6 +121,7 @@ class Rope:
             _refuse("Rope: a contiguous float32 [positions, rotary_dim] table on the device")
         self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
         self.positions, self.rotary_dim = cos_sin.shape
+        self.raw = (cos_sin.data_ptr(), self.rotary_dim, self.positions, int(self.interleaved))
 
 
 def rope_table(positions, rotary_dim, base=10000.0, device="cuda"):
@@ -133,45 +135,45 @@ def rope_table(positions, rotary_dim, base=10000.0, device="cuda"):
 
 def _rows(name, x, tokens, heads, dim, dtypes, device):
     """Token stride of a [tokens, heads, head_dim] tensor whose heads are contiguous."""
-    if x.device != device or x.dtype not in dtypes or x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != dim or \
-            (heads is not None and x.shape[1] != heads) or x.shape[1] == 0:
-        _refuse(f"{name}: wants [{tokens}, {heads if heads is not None else 'heads'}, {dim}] of {dtypes[0]} on {device}")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[1] != heads or heads == 0 or shape[2] != dim or \
+            x.dtype not in dtypes or x.device != device:
+        _refuse(f"{name}: wants [{tokens}, {heads}, {dim}] of {dtypes[0]} on {device}")
     if x.requires_grad and torch.is_grad_enabled():
         _refuse(f"{name}: has no gradient here")
     t, h, d = x.stride()
-    if d != 1 or (h != dim and x.shape[1] > 1):
+    if d != 1 or (h != dim and heads > 1):
         _refuse(f"{name}: heads are not contiguous")
-    return t if tokens > 1 else x.shape[1] * dim
+    return t if tokens > 1 else heads * dim
 
 
-class _On:
-    """The device and stream of a call: the cache's device made current, and
-    torch's current stream set to the call's, so that what the call allocates
-    belongs to it."""
+def _heads(q):
+    return q.shape[1] if q.dim() == 3 else 0
 
-    def __init__(self, cache, batch, status, stream):
-        if batch.device != cache.device:
-            _refuse("the batch is on another device than the cache")
-        if status is not None and (status.device != cache.device or status.dtype != torch.int32 or status.numel() < 1):
-            _refuse("status: an int32 tensor on the cache's device")
-        device = cache.device
-        self.guards = ()
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(device),)
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            elif stream.device != device:
-                _refuse("the stream is on another device than the cache")
-            self.guards += (torch.cuda.stream(stream),)
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
+def _check(cache, batch, status):
+    if batch.device != cache.device:
+        _refuse("the batch is on another device than the cache")
+    if status is not None and (status.device != cache.device or status.dtype != torch.int32 or status.numel() < 1):
+        _refuse("status: an int32 tensor on the cache's device")
 
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+
+def _run(call, cache, batch, stream, *args, **kw):
+    """call(handle, ...) with the stream's handle.  Where the call's device is
+    not the current one, or its stream is given, they are made torch's current
+    ones meanwhile, so that what the call allocates belongs to them."""
+    device = cache.device
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream(device).cuda_stream, cache, batch, *args, **kw)
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device != device:
+            _refuse("the stream is on another device than the cache")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream, cache, batch, *args, **kw)
 
 
 _BF16 = (torch.bfloat16, torch.int16)
@@ -186,32 +188,38 @@ def append(cache, batch, k, v, q=None, q_out=None, rope=None, q_norm=None, k_nor
     in the same pass, into q_out (allocated here unless given; q itself will
     do); rows of padding and of tokens that have no place are not written.
     Returns q_out, or None."""
+    return _run(_append, cache, batch, stream, k, v, q, q_out, rope, q_norm, k_norm, eps, status)
+
+
+def _append(stream, cache, batch, k, v, q, q_out, rope, q_norm, k_norm, eps, status):
+    _check(cache, batch, status)
     n, dim, dev = batch.total_tokens, cache.head_dim, cache.device
-    with _On(cache, batch, status, stream):
-        a = KvAppendArgs()
-        a.d_k, a.k_stride = k.data_ptr(), _rows("k", k, n, cache.kv_heads, dim, _BF16, dev)
-        a.d_v, a.v_stride = v.data_ptr(), _rows("v", v, n, cache.kv_heads, dim, _BF16, dev)
-        if q is not None:
-            a.d_q, a.q_stride, a.q_heads = q.data_ptr(), _rows("q", q, n, None, dim, _BF16, dev), q.shape[1]
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            a.d_q_out, a.q_out_stride = q_out.data_ptr(), _rows("q_out", q_out, n, q.shape[1], dim, _BF16, dev)
-        elif q_out is not None or q_norm is not None:
-            _refuse("append: q_out and q_norm go with q")
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is None:
-                continue
-            if w.shape != (dim,) or w.dtype not in _BF16 or w.device != dev or not w.is_contiguous() or \
-                    (w.requires_grad and torch.is_grad_enabled()):
-                _refuse(f"append: {name} wants BF16 [{dim}] on {dev}, without gradient")
-            setattr(a, "d_" + name, w.data_ptr())
-        a.eps = eps
-        if rope is not None:
-            if rope.cos_sin.device != dev:
-                _refuse("append: the rotation table is on another device")
-            a.d_cos_sin, a.rotary_dim, a.max_positions = rope.cos_sin.data_ptr(), rope.rotary_dim, rope.positions
-            a.interleaved = rope.interleaved
-        check(kv_append(cache.raw, batch.raw, a, status), "kv_append")
+    k_stride = _rows("k", k, n, cache.kv_heads, dim, _BF16, dev)
+    v_stride = _rows("v", v, n, cache.kv_heads, dim, _BF16, dev)
+    q_ptr = q_out_ptr = None
+    q_stride = q_out_stride = q_heads = 0
+    if q is not None:
+        q_heads = _heads(q)
+        q_stride = _rows("q", q, n, q_heads, dim, _BF16, dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out_stride = _rows("q_out", q_out, n, q_heads, dim, _BF16, dev)
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None or q_norm is not None:
+        _refuse("append: q_out and q_norm go with q")
+    for w in (q_norm, k_norm):
+        if w is not None and (w.shape != (dim,) or w.dtype not in _BF16 or w.device != dev or not w.is_contiguous() or
+                              (w.requires_grad and torch.is_grad_enabled())):
+            _refuse(f"append: norm weights want BF16 [{dim}] on {dev}, without gradient")
+    table, rotary_dim, positions, interleaved = None, 0, 0, 0
+    if rope is not None:
+        if rope.cos_sin.device != dev:
+            _refuse("append: the rotation table is on another device")
+        table, rotary_dim, positions, interleaved = rope.raw
+    a = KvAppendArgs(k.data_ptr(), v.data_ptr(), q_ptr, q_out_ptr, k_stride, v_stride, q_stride, q_out_stride, table,
+                     None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(), eps,
+                     q_heads, rotary_dim, positions, interleaved, 0)
+    check(kv_append(cache.raw, batch.raw, a, status, stream), "kv_append")
     return q_out
 
 
@@ -225,26 +233,29 @@ def attention(cache, batch, q, scale=None, causal=True, window=0, out=None, retu
     Rows of padding are not written.  workspace: a uint8 tensor of
     workspace_bytes(...) that no overlapping call uses (allocated here unless
     given)."""
-    n, dim, dev = batch.total_tokens, cache.head_dim, cache.device
-    with _On(cache, batch, status, stream):
-        a = KvAttentionArgs()
-        a.d_q, a.q_stride, a.q_heads = q.data_ptr(), _rows("q", q, n, None, dim, _BF16, dev), q.shape[1]
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        a.d_out, a.out_stride = out.data_ptr(), _rows("out", out, n, q.shape[1], dim, _BF16, dev)
-        lse = torch.empty(n, q.shape[1], dtype=torch.float32, device=dev) if return_lse else None
-        a.d_lse = lse.data_ptr() if return_lse else None
-        a.scale = dim ** -0.5 if scale is None else scale
-        if not isinstance(window, int) or not 0 <= window < 1 << 31:
-            _refuse("attention: window")
-        a.causal, a.window = bool(causal), window
+    return _run(_attention, cache, batch, stream, q, scale, causal, window, out, return_lse, workspace, status)
+
+
+def _attention(stream, cache, batch, q, scale, causal, window, out, return_lse, workspace, status):
+    _check(cache, batch, status)
+    n, dim, dev, heads = batch.total_tokens, cache.head_dim, cache.device, _heads(q)
+    q_stride = _rows("q", q, n, heads, dim, _BF16, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    out_stride = _rows("out", out, n, heads, dim, _BF16, dev)
+    if not isinstance(window, int) or not 0 <= window < 1 << 31:
+        _refuse("attention: window")
+    lse = torch.empty(n, heads, dtype=torch.float32, device=dev) if return_lse else None
+    a = KvAttentionArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None, q_stride, out_stride,
+                        dim ** -0.5 if scale is None else scale, heads, bool(causal), window)
+    if workspace is None:
         need = kv_attention_workspace_bytes(cache.raw, batch.raw, a)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            _refuse("attention: workspace wants contiguous uint8 on the cache's device")
-        check(kv_attention(cache.raw, batch.raw, a, workspace, 0 if workspace is None else workspace.numel(), status),
-              "kv_attention")
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        _refuse("attention: workspace wants contiguous uint8 on the cache's device")
+    check(kv_attention(cache.raw, batch.raw, a, workspace, 0 if workspace is None else workspace.numel(), status, stream),
+          "kv_attention")
     return (out, lse) if return_lse else out
 
 
@@ -256,32 +267,34 @@ def workspace_bytes(cache, batch, q_heads, window=0):
     return kv_attention_workspace_bytes(cache.raw, batch.raw, a)
 
 
-def _layer_dtypes(cache):
-    return tuple(t for t, d in _CACHE_DTYPES.items() if d == cache.dtype)
-
-
 def gather(cache, batch, k=None, v=None, status=None, stream=None):
     """The batch's tokens out of the pages into contiguous layer tensors
     [tokens, kv_heads, head_dim] of the cache's dtype (allocated here unless
     given), the form the codec compresses; rows of padding are not written.
     Returns (k, v)."""
-    n, dev = batch.total_tokens, cache.device
-    with _On(cache, batch, status, stream):
-        shape = (n, cache.kv_heads, cache.head_dim)
-        if k is None:
-            k = torch.empty(shape, dtype=cache.k.dtype, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=cache.k.dtype, device=dev)
-        strides = [_rows(name, x, *shape, _layer_dtypes(cache), dev) for name, x in (("k", k), ("v", v))]
-        check(kv_gather(cache.raw, batch.raw, k, strides[0], v, strides[1], status), "kv_gather")
+    return _run(_gather, cache, batch, stream, k, v, status)
+
+
+def _gather(stream, cache, batch, k, v, status):
+    _check(cache, batch, status)
+    shape, dev, dtypes = (batch.total_tokens, cache.kv_heads, cache.head_dim), cache.device, cache.dtypes
+    if k is None:
+        k = torch.empty(shape, dtype=cache.k.dtype, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=cache.k.dtype, device=dev)
+    check(kv_gather(cache.raw, batch.raw, k, _rows("k", k, *shape, dtypes, dev), v, _rows("v", v, *shape, dtypes, dev),
+                    status, stream), "kv_gather")
     return k, v
 
 
 def scatter(cache, batch, k, v, status=None, stream=None):
     """Layer tensors [tokens, kv_heads, head_dim] of the cache's dtype (as
     gather made them, or the codec decoded them) into the batch's pages."""
-    n, dev = batch.total_tokens, cache.device
-    with _On(cache, batch, status, stream):
-        strides = [_rows(name, x, n, cache.kv_heads, cache.head_dim, _layer_dtypes(cache), dev)
-                   for name, x in (("k", k), ("v", v))]
-        check(kv_scatter(cache.raw, batch.raw, k, strides[0], v, strides[1], status), "kv_scatter")
+    return _run(_scatter, cache, batch, stream, k, v, status)
+
+
+def _scatter(stream, cache, batch, k, v, status):
+    _check(cache, batch, status)
+    shape, dev, dtypes = (batch.total_tokens, cache.kv_heads, cache.head_dim), cache.device, cache.dtypes
+    check(kv_scatter(cache.raw, batch.raw, k, _rows("k", k, *shape, dtypes, dev), v, _rows("v", v, *shape, dtypes, dev),
+                     status, stream), "kv_scatter")

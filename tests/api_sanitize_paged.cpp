@@ -34,7 +34,8 @@ hipError_t launch_scatter(const CopyArgs&, hipStream_t) { ++g_launches; return h
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t) {
     ++g_launches;
     const uint64_t rows = uint64_t(a.batch.total_tokens) * a.group * a.cache.kv_heads;
-    EXPECT(tile_slots(a.batch, a.group, a.tile) * a.cache.kv_heads < (1u << 24));
+    const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
+    EXPECT((a.tile == 16 ? few_groups(slots, a.splits, a.cache.kv_heads) : slots * a.cache.kv_heads) < (1u << 24));
     EXPECT(a.splits >= 1 && a.splits <= 65535 && a.split_len % 32 == 0);
     EXPECT(uint64_t(a.splits) * a.split_len >= (a.mask.window ? 1 : a.batch.max_kv_len));
     if (a.splits > 1) EXPECT(a.part && g_workspace >= rows * a.splits * (a.cache.head_dim + 2) * 4);
