@@ -88,6 +88,13 @@ bool take_batch(const kv_batch* b, Batch& to) {
 
 bool empty(const Batch& b) { return b.num_seqs == 0 || b.total_tokens == 0; }
 
+// Workgroups of the attention's first launch in x.
+uint64_t attention_groups(const AttentionArgs& a) {
+    if (a.plan.tile == kFewRows)
+        return few_groups(a.plan.units ? a.plan.units : a.batch.num_seqs, a.cache.kv_heads);
+    return tile_slots(a.batch, a.group, a.plan.tile) * a.cache.kv_heads;
+}
+
 // Everything of kv_attention's arguments but the workspace.
 bool take_attention(const kv_cache* cache, const kv_batch* batch, const kv_attention_args* x, AttentionArgs& a) {
     if (!x || !take_cache(cache, a.cache) || !take_batch(batch, a.batch)) return false;
@@ -102,15 +109,8 @@ bool take_attention(const kv_cache* cache, const kv_batch* batch, const kv_atten
     if (!usable(x->d_q) || !usable(x->d_out) || (x->d_lse && !aligned(x->d_lse, 4)) ||
         !stride_ok(x->q_stride, row, a.batch.total_tokens, 2) || !stride_ok(x->out_stride, row, a.batch.total_tokens, 2))
         return false;
-    const AttentionPlan plan = attention_plan(a.cache.kv_heads, a.group, a.cache.head_dim, a.batch.num_seqs,
-                                              a.batch.total_tokens, a.batch.max_tokens, a.batch.max_kv_len, x->window);
-    const uint64_t slots = tile_slots(a.batch, a.group, plan.tile);
-    if (plan.tile == 16 ? few_groups(slots, plan.splits, a.cache.kv_heads) >= kMaxGroups
-                        : slots * a.cache.kv_heads >= kMaxGroups)
-        return false;
-    a.tile = plan.tile;
-    a.splits = plan.splits;
-    a.split_len = plan.split_len;
+    a.plan = attention_plan(a.cache, a.batch, a.group, x->window, a.e5m2);
+    if (attention_groups(a) >= kMaxGroups) return false;
     a.q = static_cast<const uint16_t*>(x->d_q);
     a.out = static_cast<uint16_t*>(x->d_out);
     a.lse = x->d_lse;
@@ -194,9 +194,7 @@ KV_EXPORT uint64_t kv_attention_workspace_bytes(const kv_cache* cache, const kv_
                                                 const kv_attention_args* args) {
     AttentionArgs a{};
     if (!take_attention(cache, batch, args, a) || empty(a.batch)) return 0;
-    return attention_plan(a.cache.kv_heads, a.group, a.cache.head_dim, a.batch.num_seqs, a.batch.total_tokens,
-                          a.batch.max_tokens, a.batch.max_kv_len, a.mask.window)
-        .workspace_bytes;
+    return a.plan.workspace_bytes;
 }
 
 KV_EXPORT sz_status kv_attention(const kv_cache* cache, const kv_batch* batch, const kv_attention_args* args,
@@ -204,7 +202,7 @@ KV_EXPORT sz_status kv_attention(const kv_cache* cache, const kv_batch* batch, c
     AttentionArgs a{};
     if (!take_attention(cache, batch, args, a) || (d_status && !aligned(d_status, 4))) return SZ_ERR_INVALID_ARGUMENT;
     if (empty(a.batch)) return SZ_OK;
-    const uint64_t need = kv_attention_workspace_bytes(cache, batch, args);
+    const uint64_t need = a.plan.workspace_bytes;
     if (need) {
         if (!usable(d_workspace)) return SZ_ERR_INVALID_ARGUMENT;
         if (workspace_bytes < need) return SZ_ERR_BUFFER_TOO_SMALL;
@@ -231,33 +229,46 @@ KV_EXPORT sz_status kv_scatter(const kv_cache* cache, const kv_batch* batch, con
 
 // How a call's rows and keys are cut: a function of the shapes and limits
 // that the host knows, so that the same shapes always run the same way.
-kvi::AttentionPlan kvi::attention_plan(uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint32_t num_seqs,
-                                       uint32_t total_tokens, uint32_t max_tokens, uint32_t max_kv_len,
-                                       uint32_t window) {
+kvi::AttentionPlan kvi::attention_plan(const Cache& c, const Batch& b, uint32_t group, uint32_t window, bool e5m2) {
     AttentionPlan p{};
-    const uint64_t most_rows = static_cast<uint64_t>(max_tokens) * group;
-    p.tile = most_rows <= 16 ? 16 : 128;
-    // positions that a tile can see, and tiles that the call can have
-    uint64_t range = max_kv_len;
+    const uint64_t most_rows = static_cast<uint64_t>(b.max_tokens) * group;
+    const uint64_t rows = static_cast<uint64_t>(b.total_tokens) * group;
+    p.tile = most_rows <= kFewRows ? kFewRows : 128;
+    // positions that a tile can see
+    uint64_t range = b.max_kv_len;
     if (window && static_cast<uint64_t>(window) + p.tile + 32 < range) range = static_cast<uint64_t>(window) + p.tile + 32;
     if (range == 0) range = 1;
-    const uint64_t rows = static_cast<uint64_t>(total_tokens) * group;
-    uint64_t tiles = rows / p.tile + num_seqs;
-    const uint64_t each = (most_rows + p.tile - 1) / p.tile;
-    if (num_seqs * each < tiles) tiles = num_seqs * each;
-    tiles *= kv_heads;
-    // Enough workgroups to fill the GPU, each with at least 256 positions.
-    const uint64_t kGroups = p.tile == 128 ? 512 : 1024, kLeast = 256;
-    uint64_t splits = tiles < kGroups ? (kGroups + tiles - 1) / tiles : 1;
-    const uint64_t most = (range + kLeast - 1) / kLeast;
-    if (splits > most) splits = most;
-    uint64_t len = (range + splits - 1) / splits;
-    len = (len + 127) / 128 * 128;
-    p.split_len = static_cast<uint32_t>(len);
-    p.splits = static_cast<uint32_t>((range + len - 1) / len);
-    if (p.splits > 1) {
-        const uint64_t parts = rows * kv_heads * p.splits;
-        p.workspace_bytes = sz::align256(parts * head_dim * 4) + sz::align256(parts * 8);
+    // Rows are joined by a workgroup each; where there are too many for one launch (padding among them), none is cut.
+    const bool joins = rows * c.kv_heads < kMaxGroups;
+    if (p.tile == kFewRows) {
+        p.granule = e5m2 ? 256 : 128;   // a block for each of a workgroup's waves
+        p.least = 512 / p.granule;
+        // Workgroups that run at once (2 on each of 256 CUs; by their registers 3 up to D = 80, 1 at D = 256) in
+        // one round, where a sequence is worth cutting and there are few enough of them to need it: each unit
+        // looks through all sequences.
+        const uint64_t at_once = c.head_dim <= 80 ? 768 : c.head_dim <= 128 ? 512 : 256;
+        const uint64_t most = range / p.granule + 2;
+        if (joins && range > 1024 && static_cast<uint64_t>(b.num_seqs) * c.kv_heads < 4096 && b.num_seqs * most < (uint64_t(1) << 32)) {
+            p.units = static_cast<uint32_t>(at_once / c.kv_heads / 8 * 8);
+            if (p.units == 0) p.units = 8;
+            p.parts = static_cast<uint64_t>(p.units) * c.kv_heads * 2 * kFewRows;
+        }
+    } else {
+        uint64_t tiles = rows / p.tile + b.num_seqs;
+        const uint64_t each = (most_rows + p.tile - 1) / p.tile;
+        if (b.num_seqs * each < tiles) tiles = b.num_seqs * each;
+        tiles *= c.kv_heads;
+        // Enough workgroups to fill the GPU, each with at least 256 positions.
+        constexpr uint64_t kGroups = 512, kLeast = 256;
+        uint64_t splits = joins && tiles < kGroups ? (kGroups + tiles - 1) / tiles : 1;
+        const uint64_t most = (range + kLeast - 1) / kLeast;
+        if (splits > most) splits = most;
+        uint64_t len = (range + splits - 1) / splits;
+        len = (len + 127) / 128 * 128;
+        p.split_len = static_cast<uint32_t>(len);
+        p.splits = static_cast<uint32_t>((range + len - 1) / len);
+        if (p.splits > 1) p.parts = rows * c.kv_heads * p.splits;
     }
+    if (p.parts) p.workspace_bytes = sz::align256(p.parts * (c.head_dim + 2) * 4 + p.units * 16);
     return p;
 }

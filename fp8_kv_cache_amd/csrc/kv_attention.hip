@@ -156,21 +156,21 @@ __device__ inline void wave_lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The tile of a workgroup, its fields in scalar registers.
-__device__ inline Tile my_tile(const AttentionArgs& a, uint64_t slot, uint32_t M) {
-    Tile t = wave_tile_of(a.batch, a.mask, slot, a.group, M);
-    auto scalar = [](int32_t& x) { x = __builtin_amdgcn_readfirstlane(x); };
-    scalar(t.seq.begin);
-    scalar(t.seq.n);
-    scalar(t.seq.kv);
-    scalar(t.seen);
-    scalar(t.lo);
-    scalar(t.hi);
-    scalar(t.p0);
-    scalar(t.p1);
+// A tile, the same for every lane, with its fields in scalar registers.
+__device__ inline Tile scalar(Tile t) {
+    auto one = [](int32_t& x) { x = __builtin_amdgcn_readfirstlane(x); };
+    one(t.seq.begin);
+    one(t.seq.n);
+    one(t.seq.kv);
+    one(t.seen);
+    one(t.lo);
+    one(t.hi);
+    one(t.p0);
+    one(t.p1);
     t.s = uniform(t.s);
     t.row0 = uniform(t.row0);
     t.rows = uniform(t.rows);
+    t.any = uniform(t.any);
     return t;
 }
 
@@ -218,9 +218,20 @@ __device__ inline void put_lse(const AttentionArgs& a, const RowAt& r, float m, 
             l == 0.f ? -kInf : (m + __builtin_log2f(l)) * kLn2;
 }
 
+// What a unit of the few-rows kernel leaves for k_join_few: the sequence that
+// begins in it and goes on in `more` units behind it (0: there is none):
+// (more, first token row, rows, 0)
+__device__ inline SZ_GLOBAL u32x4* cuts(const AttentionArgs& a) {
+    return reinterpret_cast<SZ_GLOBAL u32x4*>(gptr(a.part) + a.plan.parts * (a.cache.head_dim + 2));
+}
+
+// The places of a unit's KV head in the partial sums.
+__device__ inline uint64_t place_of(const AttentionArgs& a, uint32_t unit, uint32_t kv_head, uint32_t place) {
+    return (static_cast<uint64_t>(unit) * a.cache.kv_heads + kv_head) * 2 + place;
+}
+
 __device__ inline float* part_stats(const AttentionArgs& a) {
-    const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
-    return a.part + rows * a.splits * a.cache.head_dim;
+    return a.part + a.plan.parts * a.cache.head_dim;
 }
 
 // A query row's operands from BF16 to FP16, scaled by the power of two that
@@ -284,33 +295,16 @@ struct Few {
     static constexpr uint32_t kLds = kFewWaves * ((kStage > kJoin ? kStage : kJoin) + 16 * 8);
 };
 
+// One sequence's rows under one KV head over the positions [k0, k1): `whole`
+// if these are all that they see, else sums into `place`.
 template <uint32_t D, bool kE5M2>
-__global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
+__device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_t kv_head, int32_t k0, int32_t k1,
+                                  bool whole_row, uint64_t place, uint8_t* lds, uint32_t lane, uint32_t wave) {
     typedef Few<D, kE5M2> F;
     constexpr uint32_t kKeys = F::kKeys, kSub = kKeys / 16, kFrags = (D + 31) / 32, kTiles = D / 16;
     constexpr uint32_t kUnits = D * F::kSize / 16;   // 16-byte pieces of a row
     constexpr uint32_t kPer = kKeys * kUnits / 64;   // pieces of K, and of V, a lane has of a block
-    __shared__ __align__(16) uint8_t lds[F::kLds];
-    // Workgroups go to the 8 XCDs in turn.  The heads of a tile and split go
-    // to one of them, one after the other: in a token-major page their rows
-    // are neighbours, and lines that two rows share are read into one L2.
-    // The next split of a tile goes to the XCD before, so that sequences of
-    // different lengths load them alike.
-    const uint32_t turn = blockIdx.x / 8, kv_head = turn % a.cache.kv_heads;
-    const uint32_t unit = turn / a.cache.kv_heads * 8 + blockIdx.x % 8;
-    const uint32_t slots = static_cast<uint32_t>(tile_slots(a.batch, a.group, 16)), slots8 = (slots + 7) / 8 * 8;
-    const uint32_t split = unit / slots8, slot = (unit + split) % slots8;
-    if (slot >= slots) return;
-    if (kv_head == 0 && split == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 && !span_of(a.batch, slot).ok)
-        flag(a.status);
-    const Tile t = my_tile(a, slot, 16);
-    if (!t.any) return;
-    const uint32_t splits = splits_of(t, a.split_len);
-    if (split && split >= splits) return;
-    const int32_t k0 = t.lo + static_cast<int32_t>(split * a.split_len);
-    const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.split_len) ? t.hi : k0 + static_cast<int32_t>(a.split_len);
-
-    const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), g = lane / 16, c16 = lane % 16;
+    const uint32_t g = lane / 16, c16 = lane % 16;
 
     // Q^T operands: the lane's row c16, elements 32 f + 8 g ..
     const bool live = c16 < t.rows;
@@ -501,7 +495,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
             acc += r * *(KV_LDS f32x4*)(sums + (w * 16 + row) * (D + 4) + d4);
         }
         const RowAt to = row_at(t, t.row0 + row, a.group, kv_head);
-        if (splits <= 1) {
+        if (whole_row) {
             const float inv = 1.f / sum;
             f32x4 y;
 #pragma unroll
@@ -511,12 +505,60 @@ __global__ __launch_bounds__(kFewThreads, D <= 128 ? 2 : 1) void k_attend_few(At
                 __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
             if (d4 == 0) put_lse(a, to, base, sum);
         } else {
-            const uint64_t r =
-                (static_cast<uint64_t>(to.token) * (a.group * a.cache.kv_heads) + to.head) * a.splits + split;
+            const uint64_t r = place * kFewRows + row;
             *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
             if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
         }
     }
+    __syncthreads();   // the sums have been read: the next sequence's blocks may take their place
+}
+
+template <uint32_t D, bool kE5M2>
+__global__ __launch_bounds__(kFewThreads, D <= 80 ? 3 : D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
+    __shared__ __align__(16) uint8_t lds[Few<D, kE5M2>::kLds];
+    // Workgroups go to the 8 XCDs in turn.  The KV heads of a unit go to one
+    // of them, one after the other: in a token-major page their rows are
+    // neighbours, and lines that two rows share are read into one L2.
+    const uint32_t turn = blockIdx.x / 8, kv_head = turn % a.cache.kv_heads;
+    const uint32_t unit = turn / a.cache.kv_heads * 8 + blockIdx.x % 8;
+    if (kv_head == 0 && threadIdx.x == 0)
+        for (uint32_t s = unit; s < a.batch.num_seqs; s += a.plan.units ? a.plan.units : a.batch.num_seqs)
+            if (!span_of(a.batch, s).ok) flag(a.status);
+    const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+
+    // the unit's granules [start, end) of all, and the sequence s they begin in, with `before` granules before it
+    uint32_t s = unit, before = 0, start = 0, end = ~0u;
+    if (a.plan.units) {
+        const uint32_t total = wave_granules(a.batch, a.mask, a.group, a.plan.granule);
+        const uint32_t each = granules_each(total, a.plan.units, a.plan.least);
+        if (static_cast<uint64_t>(unit) * each >= total) {
+            if (unit < a.plan.units && kv_head == 0 && threadIdx.x == 0) cuts(a)[unit] = u32x4{0, 0, 0, 0};
+            return;
+        }
+        start = unit * each;
+        end = total - start < each ? total : start + each;
+        s = wave_seq_of_granule(a.batch, a.mask, a.group, a.plan.granule, start, before);
+    }
+    u32x4 cut = u32x4{0, 0, 0, 0};
+    for (; s < a.batch.num_seqs && before < end; ++s) {
+        const Tile t = scalar(tile_of_seq(a.batch, a.mask, s, a.group));
+        if (!t.any) {
+            if (!a.plan.units) return;
+            continue;
+        }
+        const uint32_t granules = granules_of(t, a.plan.granule);
+        const uint32_t from = before < start ? start - before : 0, to = end - before < granules ? end - before : granules;
+        const bool whole = from == 0 && to == granules;
+        const uint64_t place = place_of(a, unit, kv_head, before < start ? 0 : 1);
+        const int32_t k0 = t.lo + static_cast<int32_t>(from * a.plan.granule);
+        const int32_t k1 = to == granules ? t.hi : t.lo + static_cast<int32_t>(to * a.plan.granule);
+        attend_few<D, kE5M2>(a, t, kv_head, k0, k1, whole, place, lds, lane, wave);
+        if (!a.plan.units) return;
+        if (before >= start && !whole)
+            cut = u32x4{(before + granules - 1) / (end - start) - unit, static_cast<uint32_t>(t.seq.begin), t.rows, 0};
+        before += granules;
+    }
+    if (a.plan.units && kv_head == 0 && threadIdx.x == 0) cuts(a)[unit] = cut;
 }
 
 // ---- Many rows: tiles of 128 rows, 32 a wave; the 4 waves share K and V
@@ -541,12 +583,12 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
         !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
         flag(a.status);
-    const Tile t = my_tile(a, slot, M);
+    const Tile t = scalar(wave_tile_of(a.batch, a.mask, slot, a.group, M));
     if (!t.any) return;
-    const uint32_t splits = splits_of(t, a.split_len);
+    const uint32_t splits = splits_of(t, a.plan.split_len);
     if (blockIdx.y && blockIdx.y >= splits) return;
-    const int32_t k0 = t.lo + static_cast<int32_t>(blockIdx.y * a.split_len);
-    const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.split_len) ? t.hi : k0 + static_cast<int32_t>(a.split_len);
+    const int32_t k0 = t.lo + static_cast<int32_t>(blockIdx.y * a.plan.split_len);
+    const int32_t k1 = t.hi - k0 < static_cast<int32_t>(a.plan.split_len) ? t.hi : k0 + static_cast<int32_t>(a.plan.split_len);
 
     const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), half = lane / 32, c32 = lane % 32;
 
@@ -773,7 +815,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
         }
         if (live && half == 0) put_lse(a, at, base, sum);
     } else if (live) {
-        const uint64_t r = (static_cast<uint64_t>(at.token) * (a.group * a.cache.kv_heads) + at.head) * a.splits + blockIdx.y;
+        const uint64_t r = (static_cast<uint64_t>(at.token) * (a.group * a.cache.kv_heads) + at.head) * a.plan.splits + blockIdx.y;
 #pragma unroll
         for (uint32_t d = 0; d < kTiles; ++d)
 #pragma unroll
@@ -787,87 +829,97 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     }
 }
 
-// Joins the splits of each row, a row a workgroup: D / 4 lanes a split, so
-// that 3 (D = 256: 4) to 16 splits are read at a time, and a sum over them
-// through LDS.
+// A row's output from its parts, one wave a row: part z (below n) is
+// part_of(z).  The parts' weights are computed by a lane each, 64 at a time.
+template <uint32_t D, typename Part>
+__device__ inline void join_row(const AttentionArgs& a, uint32_t token, uint32_t head, uint32_t n, Part part_of) {
+    constexpr uint32_t kWide = D <= 64 ? 1 : D <= 128 ? 2 : 4;   // elements a lane
+    typedef float Vec __attribute__((ext_vector_type(kWide)));
+    typedef __bf16 Out __attribute__((ext_vector_type(kWide)));
+    const uint32_t lane = sz::lane_id(), at = lane * kWide < D ? lane * kWide : 0;
+    const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a)));
+    float base = -kInf, sum = 0.f;
+    Vec acc = Vec(0.f);
+    for (uint32_t from = 0; from < n; from += 64) {
+        const uint32_t count = n - from < 64 ? n - from : 64;
+        const f32x2 st = lane < count ? stats[part_of(from + lane)] : f32x2{-kInf, 0.f};
+        float top = st[1] != 0.f ? st[0] : -kInf;   // a part whose keys the row does not see has no maximum
+        for (uint32_t m = 32; m; m /= 2) top = fmaxf(top, __shfl_xor(top, m));
+        const float now = fmaxf(base, top), safe = now == -kInf ? 0.f : now;
+        const float keep = __builtin_amdgcn_exp2f(base - safe);
+        base = now;
+        const float weight = st[1] != 0.f ? __builtin_amdgcn_exp2f(st[0] - safe) : 0.f;
+        float add = st[1] != 0.f ? weight * st[1] : 0.f;
+        for (uint32_t m = 32; m; m /= 2) add += __shfl_xor(add, m);
+        sum = sum * keep + add;
+        acc *= keep;
+        for (uint32_t z = 0; z < count; z += 8) {   // 8 in flight; past the last, the last again, not added
+            Vec x[8];
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t part = from + (z + i < count ? z + i : count - 1);
+                x[i] = *reinterpret_cast<const SZ_GLOBAL Vec*>(gptr(a.part) + part_of(part) * D + at);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) acc += z + i < count ? __shfl(weight, z + i) * x[i] : Vec(0.f);
+        }
+    }
+    Vec y = acc / sum;
+    if (sum == 0.f) y = Vec(0.f);
+    if (lane * kWide < D)
+        *reinterpret_cast<SZ_GLOBAL Out*>(gptr(a.out) + static_cast<uint64_t>(token) * a.out_stride + head * D + at) =
+            __builtin_convertvector(y, Out);
+    if (lane == 0) put_lse(a, RowAt{token, head, 0}, base == -kInf ? 0.f : base, sum);
+}
+
 constexpr uint32_t kJoinThreads = 256;
 
+// The sequences that were cut: a workgroup has 4 rows of one unit and KV head.
 template <uint32_t D>
-__global__ __launch_bounds__(kJoinThreads) void k_join(AttentionArgs a) {
-    constexpr uint32_t kLanes = D / 4, kSets = kJoinThreads / kLanes;
-    __shared__ f32x4 sums[kSets * kLanes];
-    __shared__ float wave_top[kJoinThreads / 64], weights[kSets];
+__global__ __launch_bounds__(kJoinThreads) void k_join_few(AttentionArgs a) {
+    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads, turn = blockIdx.x / a.cache.kv_heads;
+    const uint32_t unit = turn / (kFewRows / 4), row = turn % (kFewRows / 4) * 4 + uniform(threadIdx.x / 64);
+    const u32x4 cut = cuts(a)[unit];
+    const uint32_t more = uniform(cut[0]), begin = uniform(cut[1]), rows = uniform(cut[2]);
+    if (more == 0 || row >= rows) return;
+    const uint32_t i = row / a.group;
+    join_row<D>(a, begin + i, kv_head * a.group + (row - i * a.group), more + 1, [&](uint32_t z) {
+        return place_of(a, unit + z, kv_head, z == 0 ? 1 : 0) * kFewRows + row;
+    });
+}
+
+// The splits of the tiles' rows, 4 rows a workgroup.
+template <uint32_t D>
+__global__ __launch_bounds__(kJoinThreads) void k_join_tiles(AttentionArgs a) {
     const uint32_t heads = a.group * a.cache.kv_heads;
-    const uint32_t row = blockIdx.x, token = row / heads, head = row - token * heads;
+    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * 4 + uniform(threadIdx.x / 64);
+    if (row >= static_cast<uint64_t>(a.batch.total_tokens) * heads) return;
+    const uint32_t token = uniform(static_cast<uint32_t>(row / heads)), head = uniform(static_cast<uint32_t>(row % heads));
     Tile t{};
     t.seq = span_of(a.batch, wave_seq_of_token(a.batch, token));
     if (static_cast<int32_t>(token) < t.seq.begin || static_cast<int32_t>(token) >= t.seq.begin + t.seq.n) return;
     // the tile that had the row
-    const uint32_t at = (token - t.seq.begin) * a.group + head % a.group;
-    t.row0 = at / a.tile * a.tile;
+    t.row0 = ((token - t.seq.begin) * a.group + head % a.group) / a.plan.tile * a.plan.tile;
     const uint32_t rows = static_cast<uint32_t>(t.seq.n) * a.group - t.row0;
-    t.rows = rows < a.tile ? rows : a.tile;
+    t.rows = rows < a.plan.tile ? rows : a.plan.tile;
     tile_range(t, a.mask, a.group);
-    const uint32_t splits = uniform(splits_of(t, a.split_len));
+    const uint32_t splits = uniform(splits_of(t, a.plan.split_len));
     if (splits <= 1) return;   // written by its workgroup
-
-    const uint64_t first = static_cast<uint64_t>(row) * a.splits;
-    const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a))) + first;
-    float top = -kInf;
-    for (uint32_t z = threadIdx.x; z < splits; z += kJoinThreads)
-        if (stats[z][1] != 0.f) top = fmaxf(top, stats[z][0]);
-    for (uint32_t m = 32; m; m /= 2) top = fmaxf(top, __shfl_xor(top, m));
-    if (threadIdx.x % 64 == 0) wave_top[threadIdx.x / 64] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
-    const float base = top == -kInf ? 0.f : top;
-
-    const uint32_t set = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-    if (set < kSets) {
-        const SZ_GLOBAL f32x4* part = reinterpret_cast<const SZ_GLOBAL f32x4*>(gptr(a.part) + first * D) + lane;
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        float sum = 0.f;
-#pragma unroll 4
-        for (uint32_t z = set; z < splits; z += kSets) {
-            const f32x2 st = stats[z];
-            const f32x4 x = part[z * kLanes];
-            if (st[1] != 0.f) {   // a split whose keys the row does not see has no maximum
-                const float r = __builtin_amdgcn_exp2f(st[0] - base);
-                sum += r * st[1];
-                acc += r * x;
-            }
-        }
-        sums[set * kLanes + lane] = acc;
-        if (lane == 0) weights[set] = sum;
-    }
-    __syncthreads();
-    if (threadIdx.x >= kLanes) return;
-    f32x4 acc = sums[threadIdx.x];
-    float sum = weights[0];
-    for (uint32_t i = 1; i < kSets; ++i) {
-        acc += sums[i * kLanes + threadIdx.x];
-        sum += weights[i];
-    }
-    f32x4 y;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = sum == 0.f ? 0.f : acc[j] / sum;
-    *reinterpret_cast<SZ_GLOBAL u32x2*>(gptr(a.out) + static_cast<uint64_t>(token) * a.out_stride + head * D +
-                                        threadIdx.x * 4) = __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
-    if (threadIdx.x == 0) put_lse(a, RowAt{token, head, 0}, base, sum);
+    join_row<D>(a, token, head, splits, [&](uint32_t z) { return row * a.plan.splits + z; });
 }
 
 template <uint32_t D, bool kE5M2>
 hipError_t attend(const AttentionArgs& a, hipStream_t s) {
-    const uint32_t slots = static_cast<uint32_t>(tile_slots(a.batch, a.group, a.tile));
-    if (a.tile == 16) {
-        k_attend_few<D, kE5M2><<<few_groups(slots, a.splits, a.cache.kv_heads), kFewThreads, 0, s>>>(a);
+    if (a.plan.tile == kFewRows) {
+        const uint32_t units = a.plan.units ? a.plan.units : a.batch.num_seqs;
+        k_attend_few<D, kE5M2><<<static_cast<uint32_t>(few_groups(units, a.cache.kv_heads)), kFewThreads, 0, s>>>(a);
+        if (a.plan.units)
+            k_join_few<D><<<a.plan.units * a.cache.kv_heads * (kFewRows / 4), kJoinThreads, 0, s>>>(a);
     } else {
-        const dim3 grid(slots * a.cache.kv_heads, a.splits);
+        const dim3 grid(static_cast<uint32_t>(tile_slots(a.batch, a.group, a.plan.tile)) * a.cache.kv_heads, a.plan.splits);
         k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
-    }
-    if (a.splits > 1) {
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
-        k_join<D><<<static_cast<uint32_t>(rows), kJoinThreads, 0, s>>>(a);
+        if (a.plan.splits > 1) k_join_tiles<D><<<static_cast<uint32_t>((rows + 3) / 4), kJoinThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

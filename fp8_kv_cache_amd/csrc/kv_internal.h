@@ -146,11 +146,42 @@ KV_HD uint32_t splits_of(const Tile& t, uint32_t len) {
     return t.hi > t.lo ? (static_cast<uint32_t>(t.hi - t.lo) + len - 1) / len : 0;
 }
 
-// Workgroups of the few-rows kernel: 8 tiles and splits at a time, each
-// with all KV heads.
-KV_HD uint64_t few_groups(uint64_t slots, uint64_t splits, uint64_t kv_heads) {
-    return (slots + 7) / 8 * 8 * splits * kv_heads;
+// ---- The few-rows kernel: every sequence has one tile, and its positions
+// are cut into granules.  Either a workgroup takes a whole sequence under one
+// KV head, or the granules of all sequences, one after the other, are dealt
+// to a fixed number of units in equal runs, so that the lengths, which only
+// the device knows, do not matter: a unit takes the end of one sequence, some
+// whole ones and the beginning of another.  Of the sequences in a unit at
+// most two are not whole: the one that began before it and the one that goes
+// on behind it, places 0 and 1 of its partial sums.
+constexpr uint32_t kFewRows = 16;
+
+KV_HD Tile tile_of_seq(const Batch& b, const Mask& mask, uint32_t s, uint32_t group) {
+    Tile t{};
+    t.s = s;
+    t.seq = span_of(b, s);
+    const uint64_t rows = static_cast<uint64_t>(t.seq.n) * group;
+    if (rows == 0 || rows > kFewRows) return t;
+    t.any = true;
+    t.rows = static_cast<uint32_t>(rows);
+    tile_range(t, mask, group);
+    return t;
 }
+
+// One at least, so that a sequence without keys has its rows written.
+KV_HD uint32_t granules_of(const Tile& t, uint32_t granule) {
+    if (!t.any) return 0;
+    return t.hi > t.lo ? (static_cast<uint32_t>(t.hi - t.lo) + granule - 1) / granule : 1;
+}
+
+// Granules a unit takes: `least` at least, all of `total` in `units` units.
+KV_HD uint32_t granules_each(uint32_t total, uint32_t units, uint32_t least) {
+    const uint32_t each = total / units + (total % units != 0);
+    return each < least ? least : each;
+}
+
+// Workgroups: 8 units or sequences at a time, each with all KV heads.
+KV_HD uint64_t few_groups(uint64_t units, uint64_t kv_heads) { return (units + 7) / 8 * 8 * kv_heads; }
 
 // ---- launch interfaces
 
@@ -177,6 +208,14 @@ struct CopyArgs {
     int32_t* status;
 };
 
+struct AttentionPlan {
+    uint32_t tile;                   // rows of a tile; kFewRows: the few-rows kernel
+    uint32_t splits, split_len;      // tiles: at most `splits` of split_len positions each
+    uint32_t units, granule, least;  // few rows: units (0: a workgroup a sequence), positions of a granule, granules of a unit
+    uint64_t parts;                  // partial sums of a row: tiles [row][split]; few rows [unit][KV head][2][row of the tile]
+    uint64_t workspace_bytes;
+};
+
 struct AttentionArgs {
     Cache cache;
     Batch batch;
@@ -187,19 +226,13 @@ struct AttentionArgs {
     float scale;
     Mask mask;
     uint32_t group;                  // query heads of a KV head
-    uint32_t tile;                   // rows of a tile (attention_plan)
-    uint32_t splits, split_len;      // at most `splits` of split_len positions each
-    float* part;                     // workspace: [row][split][head_dim] sums, then [row][split] (max, sum)
+    AttentionPlan plan;
+    float* part;                     // workspace: plan.parts x head_dim sums, plan.parts x (max, sum), plan.units x Cut
     int32_t* status;
     bool e5m2;
 };
 
-struct AttentionPlan {
-    uint32_t tile, splits, split_len;
-    uint64_t workspace_bytes;
-};
-AttentionPlan attention_plan(uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint32_t num_seqs, uint32_t total_tokens,
-                             uint32_t max_tokens, uint32_t max_kv_len, uint32_t window);
+AttentionPlan attention_plan(const Cache& c, const Batch& b, uint32_t group, uint32_t window, bool e5m2);
 
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 hipError_t launch_gather(const CopyArgs& a, hipStream_t s);

@@ -34,12 +34,18 @@ hipError_t launch_scatter(const CopyArgs&, hipStream_t) { ++g_launches; return h
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t) {
     ++g_launches;
     const uint64_t rows = uint64_t(a.batch.total_tokens) * a.group * a.cache.kv_heads;
-    const uint64_t slots = tile_slots(a.batch, a.group, a.tile);
-    EXPECT((a.tile == 16 ? few_groups(slots, a.splits, a.cache.kv_heads) : slots * a.cache.kv_heads) < (1u << 24));
-    EXPECT(a.splits >= 1 && a.splits <= 65535 && a.split_len % 32 == 0);
-    EXPECT(uint64_t(a.splits) * a.split_len >= (a.mask.window ? 1 : a.batch.max_kv_len));
-    if (a.splits > 1) EXPECT(a.part && g_workspace >= rows * a.splits * (a.cache.head_dim + 2) * 4);
-    if (a.splits > 1) EXPECT(rows < (1u << 24));
+    if (a.plan.tile == kFewRows) {
+        EXPECT(few_groups(a.plan.units ? a.plan.units : a.batch.num_seqs, a.cache.kv_heads) < (1u << 24));
+        EXPECT(uint64_t(a.batch.max_tokens) * a.group <= kFewRows && a.plan.granule && a.plan.least);
+        EXPECT(a.plan.parts == uint64_t(a.plan.units) * a.cache.kv_heads * 2 * kFewRows);
+        EXPECT(!a.plan.units || (uint64_t(a.batch.max_kv_len) / a.plan.granule + 1) * a.batch.num_seqs < (1ull << 32) || a.mask.window);
+    } else {
+        EXPECT(tile_slots(a.batch, a.group, a.plan.tile) * a.cache.kv_heads < (1u << 24));
+        EXPECT(a.plan.splits >= 1 && a.plan.splits <= 65535 && a.plan.split_len % 32 == 0);
+        EXPECT(uint64_t(a.plan.splits) * a.plan.split_len >= (a.mask.window ? 1 : a.batch.max_kv_len));
+        EXPECT(a.plan.parts == (a.plan.splits > 1 ? rows * a.plan.splits : 0));
+    }
+    if (a.plan.parts) EXPECT(a.part && g_workspace >= a.plan.parts * (a.cache.head_dim + 2) * 4 && rows < (1u << 24));
     return hipSuccess;
 }
 }  // namespace kvi
