@@ -270,11 +270,15 @@ __device__ inline void interleave() {
     }
 }
 
-// ---- Few rows: tiles of 16 rows, one tile, KV head and split of the keys a
-// workgroup.  Its 4 waves take blocks of keys in turn, each wave with its own
-// running maximum and sums, joined through LDS at the end.  A block goes
-// through the wave's own part of LDS as the cache has it: rows are read from
-// memory in one run each, the next block's while this one is multiplied.
+// ---- Few rows: a workgroup takes one or two KV heads of its unit's sequences
+// (kv_internal.h).  Its 4 waves, or each two of them, take blocks of keys in
+// turn, each wave with its own running maximum and sums, joined through LDS
+// at the end.  A block goes through the wave's own part of LDS as the cache
+// has it: rows are read from memory in one run each, the next block's while
+// this one is multiplied.  Bound by memory: a wave has 16 KB (D = 128) of K
+// and V on the way, 8 waves a CU.  At D = 128 in BF16, head-major pages, one
+// token of two sequences of 131072 keys is read at 6.3 TB/s, of the 7.0 that
+// a plain read without caching reaches.
 constexpr uint32_t kFewThreads = 256, kFewWaves = 4;
 
 template <uint32_t D>
@@ -295,11 +299,14 @@ struct Few {
     static constexpr uint32_t kLds = kFewWaves * ((kStage > kJoin ? kStage : kJoin) + 16 * 8);
 };
 
-// One sequence's rows under one KV head over the positions [k0, k1): `whole`
-// if these are all that they see, else sums into `place`.
-template <uint32_t D, bool kE5M2>
-__device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_t kv_head, int32_t k0, int32_t k1,
+// One sequence's rows under H neighbouring KV heads over the positions
+// [k0, k1): `whole_row` if these are all that they see, else sums into `place`
+// and, for the next head, 2 places on.
+template <uint32_t D, bool kE5M2, uint32_t H>
+__device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_t head0, int32_t k0, int32_t k1,
                                   bool whole_row, uint64_t place, uint8_t* lds, uint32_t lane, uint32_t wave) {
+    constexpr uint32_t kTeam = kFewWaves / H;   // waves of a KV head
+    const uint32_t kv_head = head0 + wave / kTeam;
     typedef Few<D, kE5M2> F;
     constexpr uint32_t kKeys = F::kKeys, kSub = kKeys / 16, kFrags = (D + 31) / 32, kTiles = D / 16;
     constexpr uint32_t kUnits = D * F::kSize / 16;   // 16-byte pieces of a row
@@ -348,8 +355,8 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
         }
     };
 
-    const int32_t step = kFewWaves * kKeys;
-    int32_t kb = k0 + static_cast<int32_t>(wave * kKeys);
+    const int32_t step = kTeam * kKeys;
+    int32_t kb = k0 + static_cast<int32_t>(wave % kTeam * kKeys);
     int32_t pages = -1, asked = -1;
     if (kb < k1) {
         pages = table.answer(kb + mine_at, table.ask(kb + mine_at));
@@ -475,26 +482,25 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     for (uint32_t d = 0; d < kTiles; ++d)
         *(KV_LDS f32x4*)(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[d];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kFewThreads) {
-        const uint32_t row = i / (D / 4), d4 = i % (D / 4) * 4;
-        if (row >= t.rows) break;
+    for (uint32_t i = threadIdx.x; i < H * t.rows * (D / 4); i += kFewThreads) {
+        const uint32_t all = i / (D / 4), d4 = i % (D / 4) * 4, team = all / t.rows, row = all - team * t.rows;
         float top = -kInf;
-        f32x2 st[kFewWaves];
+        f32x2 st[kTeam];
 #pragma unroll
-        for (uint32_t w = 0; w < kFewWaves; ++w) {
-            st[w] = stats[w * 16 + row];
+        for (uint32_t w = 0; w < kTeam; ++w) {
+            st[w] = stats[(team * kTeam + w) * 16 + row];
             top = fmaxf(top, st[w][0]);
         }
         const float base = top == -kInf ? 0.f : top;
         f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
         float sum = 0.f;
 #pragma unroll
-        for (uint32_t w = 0; w < kFewWaves; ++w) {
+        for (uint32_t w = 0; w < kTeam; ++w) {
             const float r = __builtin_amdgcn_exp2f(st[w][0] - base);
             sum += r * st[w][1];
-            acc += r * *(KV_LDS f32x4*)(sums + (w * 16 + row) * (D + 4) + d4);
+            acc += r * *(KV_LDS f32x4*)(sums + ((team * kTeam + w) * 16 + row) * (D + 4) + d4);
         }
-        const RowAt to = row_at(t, t.row0 + row, a.group, kv_head);
+        const RowAt to = row_at(t, t.row0 + row, a.group, head0 + team);
         if (whole_row) {
             const float inv = 1.f / sum;
             f32x4 y;
@@ -505,7 +511,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
                 __builtin_bit_cast(u32x2, __builtin_convertvector(y, bf16x4));
             if (d4 == 0) put_lse(a, to, base, sum);
         } else {
-            const uint64_t r = place * kFewRows + row;
+            const uint64_t r = (place + 2 * team) * kFewRows + row;
             *reinterpret_cast<SZ_GLOBAL f32x4*>(gptr(a.part) + r * D + d4) = acc;
             if (d4 == 0) *reinterpret_cast<SZ_GLOBAL f32x2*>(gptr(part_stats(a)) + 2 * r) = f32x2{base, sum};
         }
@@ -513,14 +519,14 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     __syncthreads();   // the sums have been read: the next sequence's blocks may take their place
 }
 
-template <uint32_t D, bool kE5M2>
+template <uint32_t D, bool kE5M2, uint32_t H>
 __global__ __launch_bounds__(kFewThreads, D <= 80 ? 3 : D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
     __shared__ __align__(16) uint8_t lds[Few<D, kE5M2>::kLds];
     // Workgroups go to the 8 XCDs in turn.  The KV heads of a unit go to one
     // of them, one after the other: in a token-major page their rows are
     // neighbours, and lines that two rows share are read into one L2.
-    const uint32_t turn = blockIdx.x / 8, kv_head = turn % a.cache.kv_heads;
-    const uint32_t unit = turn / a.cache.kv_heads * 8 + blockIdx.x % 8;
+    const uint32_t turn = blockIdx.x / 8, teams = a.cache.kv_heads / H, kv_head = turn % teams * H;
+    const uint32_t unit = turn / teams * 8 + blockIdx.x % 8;
     if (kv_head == 0 && threadIdx.x == 0)
         for (uint32_t s = unit; s < a.batch.num_seqs; s += a.plan.units ? a.plan.units : a.batch.num_seqs)
             if (!span_of(a.batch, s).ok) flag(a.status);
@@ -552,7 +558,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 80 ? 3 : D <= 128 ? 2 : 1) void k
         const uint64_t place = place_of(a, unit, kv_head, before < start ? 0 : 1);
         const int32_t k0 = t.lo + static_cast<int32_t>(from * a.plan.granule);
         const int32_t k1 = to == granules ? t.hi : t.lo + static_cast<int32_t>(to * a.plan.granule);
-        attend_few<D, kE5M2>(a, t, kv_head, k0, k1, whole, place, lds, lane, wave);
+        attend_few<D, kE5M2, H>(a, t, kv_head, k0, k1, whole, place, lds, lane, wave);
         if (!a.plan.units) return;
         if (before >= start && !whole)
             cut = u32x4{(before + granules - 1) / (end - start) - unit, static_cast<uint32_t>(t.seq.begin), t.rows, 0};
@@ -912,7 +918,9 @@ template <uint32_t D, bool kE5M2>
 hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     if (a.plan.tile == kFewRows) {
         const uint32_t units = a.plan.units ? a.plan.units : a.batch.num_seqs;
-        k_attend_few<D, kE5M2><<<static_cast<uint32_t>(few_groups(units, a.cache.kv_heads)), kFewThreads, 0, s>>>(a);
+        const uint32_t groups = static_cast<uint32_t>(few_groups(units, a.cache.kv_heads / a.plan.heads));
+        if (a.plan.heads == 2) k_attend_few<D, kE5M2, 2><<<groups, kFewThreads, 0, s>>>(a);
+        else k_attend_few<D, kE5M2, 1><<<groups, kFewThreads, 0, s>>>(a);
         if (a.plan.units)
             k_join_few<D><<<a.plan.units * a.cache.kv_heads * (kFewRows / 4), kJoinThreads, 0, s>>>(a);
     } else {

@@ -211,6 +211,7 @@ struct CopyArgs {
 struct AttentionPlan {
     uint32_t tile;                   // rows of a tile; kFewRows: the few-rows kernel
     uint32_t splits, split_len;      // tiles: at most `splits` of split_len positions each
+    uint32_t heads;                  // few rows: KV heads a workgroup
     uint32_t units, granule, least;  // few rows: units (0: a workgroup a sequence), positions of a granule, granules of a unit
     uint64_t parts;                  // partial sums of a row: tiles [row][split]; few rows [unit][KV head][2][row of the tile]
     uint64_t workspace_bytes;
