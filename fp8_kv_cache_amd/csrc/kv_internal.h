@@ -197,6 +197,7 @@ struct AppendArgs {
     uint32_t q_heads, rotary_dim, max_positions, interleaved;
     int32_t* status;
     bool e5m2;
+    uint32_t rows, passes;   // of a workgroup, set by the launch
 };
 
 struct CopyArgs {
@@ -206,6 +207,7 @@ struct CopyArgs {
     uint64_t k_stride, v_stride;   // bytes
     uint32_t head_bytes;
     int32_t* status;
+    uint32_t rows, lanes, pieces, head_magic;   // set by the launch
 };
 
 struct AttentionPlan {
@@ -235,7 +237,7 @@ struct AttentionArgs {
 
 AttentionPlan attention_plan(const Cache& c, const Batch& b, uint32_t group, uint32_t window, bool e5m2);
 
-hipError_t launch_append(const AppendArgs& a, hipStream_t s);
+hipError_t launch_append(AppendArgs a, hipStream_t s);
 hipError_t launch_gather(const CopyArgs& a, hipStream_t s);
 hipError_t launch_scatter(const CopyArgs& a, hipStream_t s);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);

@@ -23,7 +23,7 @@ static uint64_t g_workspace = 0;
     } while (0)
 
 namespace kvi {
-hipError_t launch_append(const AppendArgs& a, hipStream_t) {
+hipError_t launch_append(AppendArgs a, hipStream_t) {
     ++g_launches;
     EXPECT(a.batch.total_tokens > 0 && a.batch.total_tokens < (1u << 24));
     EXPECT((a.q_heads + 2 * a.cache.kv_heads + 7) / 8 <= 65535);
