@@ -29,8 +29,10 @@ int raw_value(const sz_dtype& e) {
 // Largest stride taken (elements): a pool of 2^31 pages or 2^24 rows of it
 // still has its last byte's offset inside 64 bits.
 constexpr uint64_t kMaxStride = uint64_t(1) << 31;
-// A launch has less than 2^32 threads in x: 2^24 workgroups of 256.
-constexpr uint64_t kMaxGroups = uint64_t(1) << 24;
+// A launch has less than 2^32 threads in x: 2^23 workgroups of 512.
+constexpr uint64_t kMaxGroups = uint64_t(1) << 23;
+
+constexpr uint64_t kMaxTokens = uint64_t(1) << 24;
 
 bool head_dim_ok(uint32_t d) { return d == 64 || d == 80 || d == 96 || d == 128 || d == 256; }
 
@@ -68,7 +70,7 @@ bool take_cache(const kv_cache* c, Cache& to) {
 
 bool take_batch(const kv_batch* b, Batch& to) {
     if (!b || b->reserved) return false;
-    if (b->num_seqs >= (1u << 20) || b->total_tokens >= kMaxGroups || b->max_kv_len >= (1u << 31) - (1u << 17)) return false;
+    if (b->num_seqs >= (1u << 20) || b->total_tokens >= kMaxTokens || b->max_kv_len >= (1u << 31) - (1u << 17)) return false;
     to.num_seqs = b->num_seqs;
     to.total_tokens = b->total_tokens;
     if (b->num_seqs == 0 || b->total_tokens == 0) return true;   // nothing to do: no table is read
@@ -244,10 +246,9 @@ kvi::AttentionPlan kvi::attention_plan(const Cache& c, const Batch& b, uint32_t 
         p.heads = 1;
         p.granule = e5m2 ? 256 : 128;   // a block for each of a workgroup's waves
         p.least = 512 / p.granule;
-        // Workgroups that run at once (2 on each of 256 CUs; by their registers 3 up to D = 80, 1 at D = 256) in
-        // one round, where a sequence is worth cutting and there are few enough of them to need it: each unit
-        // looks through all sequences.
-        const uint64_t at_once = c.head_dim <= 80 ? 768 : c.head_dim <= 128 ? 512 : 256;
+        // As many units as run at once on 256 CUs, in one round, where a sequence is worth cutting and there are few
+        // enough of them to need it: each unit looks through all sequences.
+        const uint64_t at_once = 256 * few_a_cu(c.head_dim, e5m2);
         const uint64_t most = range / p.granule + 2;
         if (joins && range > 1024 && static_cast<uint64_t>(b.num_seqs) * c.kv_heads < 4096 && b.num_seqs * most < (uint64_t(1) << 32)) {
             // Two heads a workgroup where their rows are neighbours in a token-major page and there are positions

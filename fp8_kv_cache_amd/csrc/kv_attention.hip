@@ -271,20 +271,18 @@ __device__ inline void interleave() {
 }
 
 // ---- Few rows: a workgroup takes one or two KV heads of its unit's sequences
-// (kv_internal.h).  Its 4 waves, or each two of them, take blocks of keys in
-// turn, each wave with its own running maximum and sums, joined through LDS
+// (kv_internal.h).  Its W waves, or each W / H of them, take blocks of keys
+// in turn, each wave with its own running maximum and sums, joined through LDS
 // at the end.  A block goes through the wave's own part of LDS as the cache
 // has it: rows are read from memory in one run each, the next block's while
 // this one is multiplied.  Bound by memory: a wave has 16 KB (D = 128) of K
 // and V on the way, 8 waves a CU.  At D = 128 in BF16, head-major pages, one
 // token of two sequences of 131072 keys is read at 6.3 TB/s, of the 7.0 that
 // a plain read without caching reaches.
-constexpr uint32_t kFewThreads = 256, kFewWaves = 4;
-
 template <uint32_t D>
 constexpr uint32_t kKeyRow = 2 * D + 16;   // rows of 16-bit K in LDS: 16-byte reads of 16 rows meet all banks
 
-template <uint32_t D, bool kE5M2>
+template <uint32_t D, bool kE5M2, uint32_t W>
 struct Few {
     static constexpr uint32_t kKeys = kE5M2 ? 64 : 32;   // a block: 16 KB of K and V either way at D = 128
     static constexpr uint32_t kSize = kE5M2 ? 1 : 2;
@@ -296,18 +294,18 @@ struct Few {
     static constexpr uint32_t kK = D * kSize + 16, kV = kE5M2 ? D + 16 : 2 * D + (D % 32 ? 0 : 32);
     static constexpr uint32_t kStage = kKeys * (kK + kV);
     static constexpr uint32_t kJoin = 16 * (D + 4) * 4;
-    static constexpr uint32_t kLds = kFewWaves * ((kStage > kJoin ? kStage : kJoin) + 16 * 8);
+    static constexpr uint32_t kLds = W * ((kStage > kJoin ? kStage : kJoin) + 16 * 8);
 };
 
 // One sequence's rows under H neighbouring KV heads over the positions
 // [k0, k1): `whole_row` if these are all that they see, else sums into `place`
 // and, for the next head, 2 places on.
-template <uint32_t D, bool kE5M2, uint32_t H>
+template <uint32_t D, bool kE5M2, uint32_t W, uint32_t H>
 __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_t head0, int32_t k0, int32_t k1,
                                   bool whole_row, uint64_t place, uint8_t* lds, uint32_t lane, uint32_t wave) {
-    constexpr uint32_t kTeam = kFewWaves / H;   // waves of a KV head
+    constexpr uint32_t kTeam = W / H;   // waves of a KV head
     const uint32_t kv_head = head0 + wave / kTeam;
-    typedef Few<D, kE5M2> F;
+    typedef Few<D, kE5M2, W> F;
     constexpr uint32_t kKeys = F::kKeys, kSub = kKeys / 16, kFrags = (D + 31) / 32, kTiles = D / 16;
     constexpr uint32_t kUnits = D * F::kSize / 16;   // 16-byte pieces of a row
     constexpr uint32_t kPer = kKeys * kUnits / 64;   // pieces of K, and of V, a lane has of a block
@@ -472,8 +470,8 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     }
     if (__any(table.bad) && lane == 0) flag(a.status);
 
-    // ---- join the 4 waves
-    KV_LDS f32x2* stats = lds_as<f32x2>((LdsBytes)lds + (F::kLds - kFewWaves * 16 * 8));   // [wave][row]
+    // ---- join the waves
+    KV_LDS f32x2* stats = lds_as<f32x2>((LdsBytes)lds + (F::kLds - W * 16 * 8));   // [wave][row]
     KV_LDS float* sums = lds_as<float>((LdsBytes)lds);                                   // [wave][row][D + 4]
     l = row_sum(l);
     __syncthreads();   // the stages have been read
@@ -482,7 +480,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     for (uint32_t d = 0; d < kTiles; ++d)
         *(KV_LDS f32x4*)(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[d];
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < H * t.rows * (D / 4); i += kFewThreads) {
+    for (uint32_t i = threadIdx.x; i < H * t.rows * (D / 4); i += 64 * W) {
         const uint32_t all = i / (D / 4), d4 = i % (D / 4) * 4, team = all / t.rows, row = all - team * t.rows;
         float top = -kInf;
         f32x2 st[kTeam];
@@ -519,9 +517,9 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     __syncthreads();   // the sums have been read: the next sequence's blocks may take their place
 }
 
-template <uint32_t D, bool kE5M2, uint32_t H>
-__global__ __launch_bounds__(kFewThreads, D <= 80 ? 3 : D <= 128 ? 2 : 1) void k_attend_few(AttentionArgs a) {
-    __shared__ __align__(16) uint8_t lds[Few<D, kE5M2>::kLds];
+template <uint32_t D, bool kE5M2, uint32_t W, uint32_t H>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : few_a_cu(D, kE5M2)) void k_attend_few(AttentionArgs a) {
+    __shared__ __align__(16) uint8_t lds[Few<D, kE5M2, W>::kLds];
     // Workgroups go to the 8 XCDs in turn.  The KV heads of a unit go to one
     // of them, one after the other: in a token-major page their rows are
     // neighbours, and lines that two rows share are read into one L2.
@@ -558,7 +556,7 @@ __global__ __launch_bounds__(kFewThreads, D <= 80 ? 3 : D <= 128 ? 2 : 1) void k
         const uint64_t place = place_of(a, unit, kv_head, before < start ? 0 : 1);
         const int32_t k0 = t.lo + static_cast<int32_t>(from * a.plan.granule);
         const int32_t k1 = to == granules ? t.hi : t.lo + static_cast<int32_t>(to * a.plan.granule);
-        attend_few<D, kE5M2, H>(a, t, kv_head, k0, k1, whole, place, lds, lane, wave);
+        attend_few<D, kE5M2, W, H>(a, t, kv_head, k0, k1, whole, place, lds, lane, wave);
         if (!a.plan.units) return;
         if (before >= start && !whole)
             cut = u32x4{(before + granules - 1) / (end - start) - unit, static_cast<uint32_t>(t.seq.begin), t.rows, 0};
@@ -919,8 +917,12 @@ hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     if (a.plan.tile == kFewRows) {
         const uint32_t units = a.plan.units ? a.plan.units : a.batch.num_seqs;
         const uint32_t groups = static_cast<uint32_t>(few_groups(units, a.cache.kv_heads / a.plan.heads));
-        if (a.plan.heads == 2) k_attend_few<D, kE5M2, 2><<<groups, kFewThreads, 0, s>>>(a);
-        else k_attend_few<D, kE5M2, 1><<<groups, kFewThreads, 0, s>>>(a);
+        // A sequence a workgroup: twice the waves, where LDS has room for their blocks (one token over 777 keys: 9
+        // us, against 14).
+        constexpr uint32_t kShort = D <= 128 ? 8 : 4;
+        if (!a.plan.units) k_attend_few<D, kE5M2, kShort, 1><<<groups, 64 * kShort, 0, s>>>(a);
+        else if (a.plan.heads == 2) k_attend_few<D, kE5M2, 4, 2><<<groups, 256, 0, s>>>(a);
+        else k_attend_few<D, kE5M2, 4, 1><<<groups, 256, 0, s>>>(a);
         if (a.plan.units)
             k_join_few<D><<<a.plan.units * a.cache.kv_heads * (kFewRows / 4), kJoinThreads, 0, s>>>(a);
     } else {

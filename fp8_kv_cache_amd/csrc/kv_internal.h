@@ -180,6 +180,11 @@ KV_HD uint32_t granules_each(uint32_t total, uint32_t units, uint32_t least) {
     return each < least ? least : each;
 }
 
+// Workgroups of 4 waves that a CU holds at once, by their registers and LDS.
+KV_HD constexpr uint32_t few_a_cu(uint32_t head_dim, bool e5m2) {
+    return head_dim <= 64 || (head_dim == 80 && !e5m2) ? 3 : head_dim <= 128 ? 2 : 1;
+}
+
 // Workgroups: 8 units or sequences at a time, each with all KV heads.
 KV_HD uint64_t few_groups(uint64_t units, uint64_t kv_heads) { return (units + 7) / 8 * 8 * kv_heads; }
 

@@ -158,13 +158,18 @@ def _check(cache, batch, status):
         _refuse("status: an int32 tensor on the cache's device")
 
 
-def _run(call, cache, batch, stream, *args, **kw):
+# the current stream's handle on a device, without an object around it where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(call, cache, batch, stream, *args):
     """call(handle, ...) with the stream's handle.  Where the call's device is
     not the current one, or its stream is given, they are made torch's current
     ones meanwhile, so that what the call allocates belongs to them."""
     device = cache.device
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(device).cuda_stream, cache, batch, *args, **kw)
+        return call(_raw_stream(device.index), cache, batch, *args)
     with torch.cuda.device(device):
         if stream is None:
             stream = torch.cuda.current_stream(device)
@@ -173,7 +178,7 @@ def _run(call, cache, batch, stream, *args, **kw):
         elif stream.device != device:
             _refuse("the stream is on another device than the cache")
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream, cache, batch, *args, **kw)
+            return call(stream.cuda_stream, cache, batch, *args)
 
 
 _BF16 = (torch.bfloat16, torch.int16)
@@ -202,7 +207,7 @@ def _append(stream, cache, batch, k, v, q, q_out, rope, q_norm, k_norm, eps, sta
         q_heads = _heads(q)
         q_stride = _rows("q", q, n, q_heads, dim, _BF16, dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         q_out_stride = _rows("q_out", q_out, n, q_heads, dim, _BF16, dev)
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None or q_norm is not None:
@@ -241,7 +246,7 @@ def _attention(stream, cache, batch, q, scale, causal, window, out, return_lse, 
     n, dim, dev, heads = batch.total_tokens, cache.head_dim, cache.device, _heads(q)
     q_stride = _rows("q", q, n, heads, dim, _BF16, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     out_stride = _rows("out", out, n, heads, dim, _BF16, dev)
     if not isinstance(window, int) or not 0 <= window < 1 << 31:
         _refuse("attention: window")
