@@ -565,18 +565,25 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : few_a_cu(D, kE5M2)) void k_att
     if (a.plan.units && kv_head == 0 && threadIdx.x == 0) cuts(a)[unit] = cut;
 }
 
-// ---- Many rows: tiles of 128 rows, 32 a wave; the 4 waves share K and V
-// tiles of N keys in LDS, two of each, so that one barrier a tile does: the
-// next tile's 16-byte pieces are on their way into registers while this one
-// is multiplied, and are put into the other buffer behind it.
-constexpr uint32_t kTileThreads = 256, kTileRows = 128;
-
+// ---- Many rows: tiles of 128 or 256 rows, 32 a wave; the 4 or 8 waves share
+// tiles of N keys and values in LDS, two of each, so that one barrier a tile
+// does: the next tile's 16-byte pieces are on their way into registers while
+// this one is multiplied, and are put into the other buffer behind it.
+// A lane's row needs 32 x D of K and of V from LDS for 4 x 32 x N x D
+// operations; with fewer rows a wave, LDS would bound it.  What bounds it is
+// the work between the products (a wave and tile of 64 keys: 1024 cycles of
+// matrix instructions, about as many of vector ones), which overlaps with the
+// other wave of the SIMD only in part: 2048 new of 8192 keys at D = 128, 32
+// query heads, 276 us in tiles of 256 rows, 873 TFLOP/s of the 1330 that a
+// large library product reaches here.  Taking turns by barriers (one half of
+// the workgroup multiplies while the other computes weights) measured the
+// same as two workgroups left alone, 298 us.
 template <uint32_t D>
 constexpr uint32_t kValueRow = ((2 * D + 63) / 64 | 1) * 64;      // V rows: 4 rows of 64 bytes meet all banks
 
-template <uint32_t D, bool kE5M2, uint32_t N>
-__global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(AttentionArgs a) {
-    constexpr uint32_t M = kTileRows, kFrags = D / 16, kTiles = (D + 31) / 32, kSub = N / 32;
+template <uint32_t D, bool kE5M2, uint32_t N, uint32_t W>
+__global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(AttentionArgs a) {
+    constexpr uint32_t M = 32 * W, kTileThreads = 64 * W, kFrags = D / 16, kTiles = (D + 31) / 32, kSub = N / 32;
     constexpr uint32_t kSize = kE5M2 ? 1 : 2, kUnits = D * kSize / 16;   // 16-byte pieces of a row of the cache
     constexpr uint32_t kPieces = N * kUnits, kPer = (kPieces + kTileThreads - 1) / kTileThreads;
     constexpr uint32_t kBuffer = N * (kKeyRow<D> + kValueRow<D>);
@@ -630,18 +637,25 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     Pages table(a, t, k1);
     const int32_t mine_at = static_cast<int32_t>(lane % N);   // the key whose page this lane looks up
     u32x4 kreg[kPer], vreg[kPer];
-    uint64_t off[kPer];   // where the thread's pieces of the tile are; keys without a page are loaded from page 0
-    auto find = [&](int32_t kb, int32_t pages) {
+    // Tiles begin at multiples of N, so a key's slot is its own part of it, the same in every tile, and in pages of
+    // more than a tile the tile's first slot.
+    const uint32_t page_mask = (1u << a.cache.log2_page) - 1;
+    uint64_t own[kPer];
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        const uint32_t u = threadIdx.x + kTileThreads * j;
+        own[j] = (u / kUnits % N & page_mask) * a.cache.token_stride + u % kUnits * 16;
+    }
+    // Keys without a page are loaded from page 0: their scores are masked, their values get weight 0.
+    auto load = [&](int32_t kb, int32_t pages) {
+        const uint64_t first_slot = (static_cast<uint32_t>(kb) & page_mask & ~(N - 1)) * a.cache.token_stride;
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j) {
-            const uint32_t u = threadIdx.x + kTileThreads * j, key = u / kUnits % N, col = u % kUnits;
-            const int32_t page = __shfl(pages, key);
-            off[j] = slot_offset(a.cache, page < 0 ? 0 : page, kb + static_cast<int32_t>(key)) + col * 16;
+            const int32_t page = __shfl(pages, (threadIdx.x + kTileThreads * j) / kUnits % N);
+            const uint64_t off = static_cast<uint32_t>(page < 0 ? 0 : page) * a.cache.page_stride + (own[j] + first_slot);
+            kreg[j] = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_k + off);
+            vreg[j] = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool_v + off);
         }
-    };
-    auto load = [&](u32x4* to, const SZ_GLOBAL uint8_t* pool) {
-#pragma unroll
-        for (uint32_t j = 0; j < kPer; ++j) to[j] = *reinterpret_cast<const SZ_GLOBAL u32x4*>(pool + off[j]);
     };
     // Rows of the tile all see all of [all_from, all_to); a tile of keys that
     // is not inside, or has keys without a page, is an edge.
@@ -685,9 +699,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
     if (k0 < k1) {
         pages = table.answer(k0 + mine_at, table.ask(k0 + mine_at));
         asked = table.ask(k0 + kStep + mine_at);
-        find(k0, pages);
-        load(kreg, pool_k);
-        load(vreg, pool_v);
+        load(k0, pages);
         if (threadIdx.x < 2) marks[threadIdx.x] = -1;
         __syncthreads();
         put(0, k0, is_edge(k0, __ballot(pages >= 0)));
@@ -699,12 +711,12 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
         const uint64_t here = __ballot(pages >= 0);   // bit key: it has a page
         const LdsBytes buffer = (LdsBytes)lds + turn * kBuffer;
         __syncthreads();   // this tile is in LDS; the other buffer has been read by every wave
-        if (more) {
+        auto fetch = [&] {
+            if (!more) return;
             pages = table.answer(kb + kStep + mine_at, asked);
             asked = table.ask(kb + 2 * kStep + mine_at);
-            find(kb + kStep, pages);
-            load(kreg, pool_k);
-        }
+            load(kb + kStep, pages);
+        };
         if (kb < any_to && kb + kStep > any_from) {
             f32x16 s[kSub];
 #pragma unroll
@@ -719,7 +731,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                     s[kt] = mfma32<kE5M2>(x, q[f], s[kt]);
                 }
             interleave<kFrags * kSub, 1, 4>();
-            if (more) load(vreg, pool_v);
+            fetch();   // behind the first product: its operands' registers are then free
             const bool whole = here == ~0ull && kb >= all_from && kb + kStep <= all_to;
             if (!whole) {
                 const int32_t from = first - kb - static_cast<int32_t>(4 * half), to = last - kb - static_cast<int32_t>(4 * half);
@@ -760,6 +772,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
             };
             const LdsBytes values = buffer + N * kKeyRow<D>;
             const LdsBytes read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
+            __builtin_amdgcn_s_setprio(1);   // ahead of a wave that is at its scores: 6% at 2048 new of 8192
 #pragma unroll
             for (uint32_t kk = 0; kk < 2 * kSub; ++kk) {
                 const u32x4 p = weights(kk);
@@ -771,6 +784,7 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                 }
             }
             interleave<2 * kSub * kTiles, 2, 4>();
+            __builtin_amdgcn_s_setprio(0);
             if (is_edge(kb, here) && marks[turn] == kb) {   // Inf and NaN, to the rows that see them
 #pragma unroll 1
                 for (uint32_t key = 0; key < N; ++key) {
@@ -789,8 +803,8 @@ __global__ __launch_bounds__(kTileThreads, D <= 128 ? 2 : 1) void k_attend_tile(
                         }
                 }
             }
-        } else if (more) {
-            load(vreg, pool_v);
+        } else {
+            fetch();
         }
         if (more) put(turn ^ 1, kb + kStep, is_edge(kb + kStep, __ballot(pages >= 0)));
     }
@@ -927,7 +941,12 @@ hipError_t attend(const AttentionArgs& a, hipStream_t s) {
             k_join_few<D><<<a.plan.units * a.cache.kv_heads * (kFewRows / 4), kJoinThreads, 0, s>>>(a);
     } else {
         const dim3 grid(static_cast<uint32_t>(tile_slots(a.batch, a.group, a.plan.tile)) * a.cache.kv_heads, a.plan.splits);
-        k_attend_tile<D, kE5M2, D <= 128 ? 64 : 32><<<grid, kTileThreads, 0, s>>>(a);
+        if constexpr (D <= 128) {
+            if (a.plan.tile == 256) k_attend_tile<D, kE5M2, 64, 8><<<grid, 512, 0, s>>>(a);
+            else k_attend_tile<D, kE5M2, 64, 4><<<grid, 256, 0, s>>>(a);
+        } else {
+            k_attend_tile<D, kE5M2, 32, 4><<<grid, 256, 0, s>>>(a);
+        }
         const uint64_t rows = static_cast<uint64_t>(a.batch.total_tokens) * a.group * a.cache.kv_heads;
         if (a.plan.splits > 1) k_join_tiles<D><<<static_cast<uint32_t>((rows + 3) / 4), kJoinThreads, 0, s>>>(a);
     }

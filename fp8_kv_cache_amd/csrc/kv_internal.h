@@ -92,7 +92,7 @@ struct Tile {
     Span seq;
     uint32_t s;
     uint32_t row0, rows;      // first row of the tile in the sequence, and how many
-    int32_t seen, lo, hi;     // positions that any of its rows sees: [seen, hi); lo is seen, down to a multiple of 32
+    int32_t seen, lo, hi;     // positions that any of its rows sees: [seen, hi); lo is seen, down to a multiple of 64
     int32_t p0, p1;           // positions of its first and last token
     bool any;
 };
@@ -110,7 +110,7 @@ KV_HD void tile_range(Tile& t, const Mask& mask, uint32_t group) {
     t.p0 = t.seq.first() + static_cast<int32_t>(t.row0 / group);
     t.p1 = t.seq.first() + static_cast<int32_t>((t.row0 + t.rows - 1) / group);
     t.seen = mask.first(t.p0);
-    t.lo = t.seen & ~31;
+    t.lo = t.seen & ~63;
     t.hi = mask.last(t.p1, t.seq.kv);
 }
 

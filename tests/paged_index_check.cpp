@@ -91,7 +91,7 @@ int main() {
                         if (hi > lo) CHECK(lo >= t.seen && hi <= t.hi);
                         CHECK(hi <= t.seq.kv);
                     }
-                    CHECK(t.lo % 32 == 0 && t.lo <= t.seen && t.lo > t.seen - 32 && t.lo >= 0);
+                    CHECK(t.lo % 64 == 0 && t.lo <= t.seen && t.lo > t.seen - 64 && t.lo >= 0);
                     const uint32_t len = 128u << upto(3), splits = splits_of(t, len);
                     if (t.hi > t.lo)
                         CHECK(t.lo + static_cast<int64_t>(splits) * len >= t.hi && t.lo + static_cast<int64_t>(splits - 1) * len < t.hi);

@@ -677,3 +677,21 @@ def test_transfer_between_paged_caches(paged, dtype, compressed):
             assert torch.equal(bits(x), bits(y))
     with pytest.raises(ValueError):
         link.ship(caches[:2], batch, targets[:2], its_batch)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("new,kv,window", [([150, 90], [151, 400], 0), ([70, 129], [70, 777], 100), ([260], [64 * 5], 0)])
+def test_long_chunks(paged, dim, dtype, new, kv, window):
+    """More rows a sequence than the smaller tiles take; one key tile, two,
+    and odd and even numbers of them."""
+    say("long chunks", dim, dtype, new, kv, window)
+    check_attention(paged, Setup(new, kv, 1, dim, dtype, pad=1, seed=dim), 4, window=window)
+
+
+@pytest.mark.parametrize("keys", [1, 63, 64, 65, 127, 128, 129, 192, 193])
+def test_key_tiles_at_their_edges(paged, keys):
+    say("key tiles", keys)
+    for new in (20, 40, 100):
+        check_attention(paged, Setup([new], [keys], 1, 64, BF16, seed=keys), 8)
+        check_attention(paged, Setup([new], [keys], 1, 64, E5M2, seed=keys), 8, causal=False)
