@@ -590,7 +590,8 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
     __shared__ __align__(16) uint8_t lds[2 * kBuffer];
     __shared__ int32_t marks[2];   // first key of the tile in each buffer, if Inf or NaN were left out of it
     const uint32_t kv_head = blockIdx.x % a.cache.kv_heads;
-    const uint64_t slot = blockIdx.x / a.cache.kv_heads;
+    // a sequence's last tiles, which see the most keys, first
+    const uint64_t slot = (gridDim.x - 1 - blockIdx.x) / a.cache.kv_heads;
     if (kv_head == 0 && blockIdx.y == 0 && slot < a.batch.num_seqs && threadIdx.x == 0 &&
         !span_of(a.batch, static_cast<uint32_t>(slot)).ok)
         flag(a.status);
