@@ -145,9 +145,15 @@ __device__ inline void add_not_finite(const SZ_GLOBAL uint8_t* from, float* o) {
     }
 }
 
-// How far a row's maximum may pass the one its sums are scaled by before
-// they are rescaled: the weights stay below 2^8, exact in every type here.
-constexpr float kSlack = 8.f;
+// How far (powers of two) a row's maximum may pass the one its sums are
+// scaled by before they are rescaled.  FP16 weights lose nothing by it (2 x
+// 1000 of 12345 E5M2 keys: 667 us, 694 without).  BF16 ones do: scaled by the
+// maximum itself, the largest weight is 1 and is not rounded, and the error
+// of peaked rows is a quarter smaller (0.0018 of the result's norm at 64 x 1
+// to 8192 keys, 0.0023 with this at 8), which is worth the 4% it takes of
+// long chunks (2048 new of 8192: 289 us, 278) and nothing elsewhere.
+template <bool kE5M2>
+constexpr float kSlack = kE5M2 ? 8.f : 0.f;
 
 // LDS order inside one wave: its LDS instructions execute in order; this
 // keeps the compiler from moving one lane's reads over another's writes.
@@ -418,7 +424,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
 #pragma unroll
         for (uint32_t i = 1; i < 4 * kSub; ++i) top = fmaxf(top, s[i / 4][i % 4]);
         top = row_max(top) * c;
-        if (__any(top > m + kSlack)) {
+        if (__any(top > m + kSlack<kE5M2>)) {
             const float now = fmaxf(m, top), r = now == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - now);
             m = now;
             l *= r;
@@ -752,7 +758,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
 #pragma unroll
             for (uint32_t i = 1; i < 16 * kSub; ++i) top = fmaxf(top, s[i / 16][i % 16]);
             top = fmaxf(swap32(top, false), swap32(top, true)) * c;
-            if (__any(top > m + kSlack)) {
+            if (__any(top > m + kSlack<kE5M2>)) {
                 const float now = fmaxf(m, top), r = now == -kInf ? 1.f : __builtin_amdgcn_exp2f(m - now);
                 m = now;
                 l *= r;
