@@ -695,3 +695,159 @@ def test_key_tiles_at_their_edges(paged, keys):
     for new in (20, 40, 100):
         check_attention(paged, Setup([new], [keys], 1, 64, BF16, seed=keys), 8)
         check_attention(paged, Setup([new], [keys], 1, 64, E5M2, seed=keys), 8, causal=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("head_major", [False, True])
+@pytest.mark.parametrize("dim,heads", [(64, 4), (80, 2), (96, 3), (128, 8), (128, 1), (256, 2)])
+def test_bounds_far_above_the_lengths(paged, dim, heads, head_major, dtype):
+    """max_kv_len and max_tokens bound the device's lengths and choose how
+    the work is cut; whatever they are, the result is the lengths'."""
+    say("bounds", dim, heads, head_major, dtype)
+    new, kv = [1, 2, 1, 0, 1, 1], [700, 40, 1, 9, 0, 2100]
+    st = Setup(new, kv, heads, dim, dtype, head_major=head_major, pad=2, seed=dim)
+    q = st.rows(2 * heads)
+    for max_tokens, max_kv in ((2, 2100), (2, 5000), (2, 300000), (3, 10 ** 9), (70, 2100), (70, 300000), (2000, 10 ** 9)):
+        cache, batch, status = handles(paged, st, max_tokens, max_kv)
+        check_attention(paged, st, 2 * heads, q=q, handle=(cache, batch, status))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("max_kv", [8, 3000])
+def test_thousands_of_sequences(paged, max_kv, dtype):
+    """More sequences than two steps of the search tell apart."""
+    say("thousands", max_kv, dtype)
+    g = torch.Generator().manual_seed(7)
+    kv = torch.randint(0, 9, (5000,), generator=g).tolist()
+    new = [int(min(n, 1)) for n in kv]
+    st = Setup(new, kv, 1, 64, dtype, page=8, pad=3, seed=1)
+    check_attention(paged, st, 1, handle=handles(paged, st, 1, max_kv))
+    cache, batch, status = handles(paged, st)
+    k, _ = paged.gather(cache, batch, status=status)
+    rows = [(row, st.place(s, p)) for row, s, p in st.tokens()]
+    assert torch.equal(bits(down(k))[[r for r, _ in rows]],
+                       torch.stack([bits(st.k)[page, slot] for _, (page, slot) in rows]))
+
+
+def test_rows_before_the_first_sequence(paged):
+    """cu_tokens may begin past 0: the rows before are padding too."""
+    say("leading padding")
+    st = Setup([3, 2], [40, 70], 2, 64, BF16)
+    q, k, v = st.rows(4).cuda(), st.rows(2).cuda(), st.rows(2).cuda()
+    cache, batch, status = handles(paged, st)
+    want = paged.attention(cache, batch, q)
+    moved = paged.PageBatch(st.table.cuda(), (st.cu + 4).cuda(), st.kv_lens.cuda(), 10, 3, 70)
+
+    def pad(x):
+        return torch.cat([torch.full_like(x[:4], math.nan), x, torch.full_like(x[:1], math.nan)])
+    out = marked((10, 4, 64))
+    paged.attention(cache, moved, pad(q), out=out, status=status)
+    assert torch.equal(out[4:9], want) and (out[:4].contiguous().view(torch.uint8) == MARK).all()
+    a, b = paged.gather(cache, batch)
+    c, d = marked((10, 2, 64)), marked((10, 2, 64))
+    paged.gather(cache, moved, c, d, status=status)
+    assert torch.equal(c[4:9], a) and (c[:4].contiguous().view(torch.uint8) == MARK).all() and (d[9:].view(torch.uint8) == MARK).all()
+    paged.append(cache, moved, pad(k), pad(v), status=status)
+    assert torch.equal(paged.gather(cache, batch)[1], v) and int(status) == 0
+
+
+def test_shared_pages_and_output_in_the_query(paged):
+    """Two sequences with the same pages (a common prompt); out = q."""
+    say("shared pages")
+    st = Setup([1, 30], [90, 100], 2, 128, BF16)
+    st.table[0] = st.table[1]
+    q = st.rows(8)
+    got = check_attention(paged, st, 8, q=q)
+    cache, batch, _ = handles(paged, st)
+    dev = q.cuda()
+    paged.attention(cache, batch, dev, out=dev)
+    assert torch.equal(down(dev).double(), got)
+
+
+def test_null_stream_handle(paged):
+    say("stream 0")
+    st = Setup([1], [300], 2, 128, BF16)
+    q = st.rows(8).cuda()
+    cache, batch, _ = handles(paged, st)
+    want = paged.attention(cache, batch, q)
+    torch.cuda.synchronize()
+    got = paged.attention(cache, batch, q, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_the_tensor_layer_refuses(paged):
+    """Shapes, types, layouts, places and gradients that the calls do not take."""
+    from fp8_kv_cache_amd import SzError
+    say("refusals")
+    st = Setup([2], [40], 2, 64, BF16)
+    cache, batch, _ = handles(paged, st)
+    k, q = st.rows(2).cuda(), st.rows(4).cuda()
+    rope = paged.Rope(paged.rope_table(40, 64))
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    bad = [lambda: paged.attention(cache, batch, q[:1]), lambda: paged.attention(cache, batch, q.float()),
+           lambda: paged.attention(cache, batch, q.cpu()), lambda: paged.attention(cache, batch, q[..., ::2]),
+           lambda: paged.attention(cache, batch, q[:, :3]), lambda: paged.attention(cache, batch, q[:, 0]),
+           lambda: paged.attention(cache, batch, q.transpose(0, 1).contiguous().transpose(0, 1)),
+           lambda: paged.attention(cache, batch, q.clone().requires_grad_()),
+           lambda: paged.attention(cache, batch, q, out=torch.empty_like(q[:, :2])),
+           lambda: paged.attention(cache, batch, q, scale=0.0), lambda: paged.attention(cache, batch, q, scale=math.nan),
+           lambda: paged.attention(cache, batch, q, window=-1), lambda: paged.attention(cache, batch, q, window=5, causal=False),
+           lambda: paged.attention(cache, batch, q, status=torch.zeros(1, device="cuda")),
+           lambda: paged.attention(cache, batch, q, workspace=torch.zeros(4, device="cuda")),
+           lambda: paged.append(cache, batch, k, k[:1]), lambda: paged.append(cache, batch, k, k, q_out=q),
+           lambda: paged.append(cache, batch, k, k, q_norm=w), lambda: paged.append(cache, batch, k, k, k_norm=w[:32]),
+           lambda: paged.append(cache, batch, k, k, k_norm=w, eps=-1.0),
+           lambda: paged.append(cache, batch, k, k, rope=paged.Rope(paged.rope_table(40, 96))),
+           lambda: paged.append(cache, batch, k, k, rope=paged.Rope(paged.rope_table(40, 24))),
+           lambda: paged.gather(cache, batch, k, k.to(torch.float8_e5m2)), lambda: paged.scatter(cache, batch, k, k[:, :1]),
+           lambda: paged.scatter(cache, batch, k, k.float()),
+           lambda: paged.PagedCache(cache.k[..., :48], cache.v[..., :48]) and paged.gather(
+               paged.PagedCache(cache.k[..., :48], cache.v[..., :48]), batch),
+           lambda: paged.PagedCache(cache.k, cache.v.transpose(1, 2)), lambda: paged.PagedCache(cache.k.half(), cache.v.half()),
+           lambda: paged.PagedCache(cache.k, cache.v.contiguous()[:, :8]),
+           lambda: paged.PageBatch(st.table.cuda().long(), st.cu.cuda(), st.kv_lens.cuda()),
+           lambda: paged.PageBatch(st.table.cuda(), st.cu.cuda()[:1], st.kv_lens.cuda()),
+           lambda: paged.PageBatch(st.table.cuda(), st.cu.cuda(), st.kv_lens.cuda(), -1),
+           lambda: paged.Rope(torch.zeros(4, 64, device="cuda").half())]
+    for i, call in enumerate(bad):
+        with pytest.raises(SzError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    assert paged.append(cache, batch, k, k, q=q, rope=rope, q_norm=w, k_norm=w).shape == q.shape
+
+
+def test_lengths_read_from_the_device(paged):
+    say("read lengths")
+    st = Setup([2, 5], [40, 9], 2, 64, BF16)
+    cache = paged.PagedCache(up(st.k), up(st.v))
+    batch = paged.PageBatch(st.table.cuda(), st.cu.cuda(), st.kv_lens.cuda())
+    assert (batch.total_tokens, batch.raw.max_tokens, batch.raw.max_kv_len) == (7, 5, 40)
+    check_attention(paged, st, 4, handle=(cache, batch, torch.zeros(1, dtype=torch.int32, device="cuda")))
+
+
+def test_two_graphs_and_eager_work_side_by_side(paged):
+    """Two captured attentions with workspaces of their own, replayed on two
+    streams at once, with eager calls between."""
+    say("two graphs")
+    st = Setup([1, 1], [3000, 2500], 2, 128, BF16, page=64)
+    cache, batch, _ = handles(paged, st)
+    qs = [st.rows(8).cuda() for _ in range(2)]
+    want = [paged.attention(cache, batch, q) for q in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    graphs = [torch.cuda.CUDAGraph() for _ in qs]
+    for graph, q, out in zip(graphs, qs, outs):
+        space = torch.empty(paged.workspace_bytes(cache, batch, 8), dtype=torch.uint8, device="cuda")
+        with torch.cuda.graph(graph):
+            paged.attention(cache, batch, q, out=out, workspace=space)
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(4):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = paged.attention(cache, batch, qs[0])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, want[0])
