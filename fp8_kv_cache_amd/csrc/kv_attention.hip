@@ -293,8 +293,8 @@ struct Few {
     static constexpr uint32_t kKeys = kE5M2 ? 64 : 32;   // a block: 16 KB of K and V either way at D = 128
     static constexpr uint32_t kSize = kE5M2 ? 1 : 2;
     // Rows of whole 128-byte lines are read once and kept in no cache (64 x 1
-    // to 8192 keys: 255 us, against 277 with plain loads); neighbouring heads
-    // share the lines of others (D = 80, 32 x 5 tokens: 115 us plain, 129).
+    // to 8192 keys: 213 us, against 238 with plain loads); neighbouring heads
+    // share the lines of others (D = 80, 32 x 5 tokens: 108 us plain, 118).
     static constexpr bool kOwnLines = D * kSize % 128 == 0;
     // rows in LDS; BF16 V: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
     static constexpr uint32_t kK = D * kSize + 16, kV = kE5M2 ? D + 16 : 2 * D + (D % 32 ? 0 : 32);
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : few_a_cu(D, kE5M2)) void k_att
 // the work between the products (a wave and tile of 64 keys: 1024 cycles of
 // matrix instructions, about as many of vector ones), which overlaps with the
 // other wave of the SIMD only in part: 2048 new of 8192 keys at D = 128, 32
-// query heads, 276 us in tiles of 256 rows, 873 TFLOP/s of the 1330 that a
+// query heads, 276 us in tiles of 256 rows, 871 TFLOP/s of the 1330 that a
 // large library product reaches here.  Taking turns by barriers (one half of
 // the workgroup multiplies while the other computes weights) measured the
 // same as two workgroups left alone, 298 us.
@@ -865,9 +865,19 @@ __device__ inline void join_row(const AttentionArgs& a, uint32_t token, uint32_t
     const SZ_GLOBAL f32x2* stats = reinterpret_cast<const SZ_GLOBAL f32x2*>(gptr(part_stats(a)));
     float base = -kInf, sum = 0.f;
     Vec acc = Vec(0.f);
+    constexpr uint32_t kAhead = 8;   // parts in flight; past the last, the last again, not added
     for (uint32_t from = 0; from < n; from += 64) {
         const uint32_t count = n - from < 64 ? n - from : 64;
         const f32x2 st = lane < count ? stats[part_of(from + lane)] : f32x2{-kInf, 0.f};
+        Vec x[kAhead];
+        auto take = [&](uint32_t z) {
+#pragma unroll
+            for (uint32_t i = 0; i < kAhead; ++i) {
+                const uint32_t part = from + (z + i < count ? z + i : count - 1);
+                x[i] = *reinterpret_cast<const SZ_GLOBAL Vec*>(gptr(a.part) + part_of(part) * D + at);
+            }
+        };
+        take(0);
         float top = st[1] != 0.f ? st[0] : -kInf;   // a part whose keys the row does not see has no maximum
         for (uint32_t m = 32; m; m /= 2) top = fmaxf(top, __shfl_xor(top, m));
         const float now = fmaxf(base, top), safe = now == -kInf ? 0.f : now;
@@ -878,15 +888,10 @@ __device__ inline void join_row(const AttentionArgs& a, uint32_t token, uint32_t
         for (uint32_t m = 32; m; m /= 2) add += __shfl_xor(add, m);
         sum = sum * keep + add;
         acc *= keep;
-        for (uint32_t z = 0; z < count; z += 8) {   // 8 in flight; past the last, the last again, not added
-            Vec x[8];
+        for (uint32_t z = 0; z < count; z += kAhead) {
+            if (z) take(z);
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const uint32_t part = from + (z + i < count ? z + i : count - 1);
-                x[i] = *reinterpret_cast<const SZ_GLOBAL Vec*>(gptr(a.part) + part_of(part) * D + at);
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) acc += z + i < count ? __shfl(weight, z + i) * x[i] : Vec(0.f);
+            for (uint32_t i = 0; i < kAhead; ++i) acc += z + i < count ? __shfl(weight, z + i) * x[i] : Vec(0.f);
         }
     }
     Vec y = acc / sum;
@@ -902,8 +907,8 @@ constexpr uint32_t kJoinThreads = 256;
 // The sequences that were cut: a workgroup has 4 rows of one unit and KV head.
 template <uint32_t D>
 __global__ __launch_bounds__(kJoinThreads) void k_join_few(AttentionArgs a) {
-    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads, turn = blockIdx.x / a.cache.kv_heads;
-    const uint32_t unit = turn / (kFewRows / 4), row = turn % (kFewRows / 4) * 4 + uniform(threadIdx.x / 64);
+    const uint32_t kv_head = blockIdx.x % a.cache.kv_heads, unit = blockIdx.x / a.cache.kv_heads;
+    const uint32_t row = blockIdx.y * 4 + uniform(threadIdx.x / 64);
     const u32x4 cut = cuts(a)[unit];
     const uint32_t more = uniform(cut[0]), begin = uniform(cut[1]), rows = uniform(cut[2]);
     if (more == 0 || row >= rows) return;
@@ -938,14 +943,16 @@ hipError_t attend(const AttentionArgs& a, hipStream_t s) {
     if (a.plan.tile == kFewRows) {
         const uint32_t units = a.plan.units ? a.plan.units : a.batch.num_seqs;
         const uint32_t groups = static_cast<uint32_t>(few_groups(units, a.cache.kv_heads / a.plan.heads));
-        // A sequence a workgroup: twice the waves, where LDS has room for their blocks (one token over 777 keys: 9
-        // us, against 14).
+        // A sequence a workgroup: twice the waves where the GPU is not full and LDS has room for their blocks (one
+        // token over 777 keys: 13.3 us in a graph, 15.5 with 4; 256 sequences of up to 1000: 121, 111).
         constexpr uint32_t kShort = D <= 128 ? 8 : 4;
-        if (!a.plan.units) k_attend_few<D, kE5M2, kShort, 1><<<groups, 64 * kShort, 0, s>>>(a);
+        if (!a.plan.units && a.batch.num_seqs * a.cache.kv_heads <= 256)
+            k_attend_few<D, kE5M2, kShort, 1><<<groups, 64 * kShort, 0, s>>>(a);
+        else if (!a.plan.units) k_attend_few<D, kE5M2, 4, 1><<<groups, 256, 0, s>>>(a);
         else if (a.plan.heads == 2) k_attend_few<D, kE5M2, 4, 2><<<groups, 256, 0, s>>>(a);
         else k_attend_few<D, kE5M2, 4, 1><<<groups, 256, 0, s>>>(a);
         if (a.plan.units)
-            k_join_few<D><<<a.plan.units * a.cache.kv_heads * (kFewRows / 4), kJoinThreads, 0, s>>>(a);
+            k_join_few<D><<<dim3(a.plan.units * a.cache.kv_heads, (a.batch.max_tokens * a.group + 3) / 4), kJoinThreads, 0, s>>>(a);
     } else {
         const dim3 grid(static_cast<uint32_t>(tile_slots(a.batch, a.group, a.plan.tile)) * a.cache.kv_heads, a.plan.splits);
         if constexpr (D <= 128) {
