@@ -234,7 +234,7 @@ def attention(cache, batch, q, scale=None, causal=True, window=0, out=None, retu
     BF16, their keys and values appended before) over the cache.  scale
     defaults to head_dim ** -0.5.  window > 0: a token sees itself and the
     window - 1 positions before it.  Returns out (BF16, q's shape; allocated
-    here unless given), with return_lse (out, lse float32 [tokens, q_heads]).
+    here unless given; q itself will do), with return_lse (out, lse float32 [tokens, q_heads]).
     Rows of padding are not written.  workspace: a uint8 tensor of
     workspace_bytes(...) that no overlapping call uses (allocated here unless
     given)."""

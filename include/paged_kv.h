@@ -136,6 +136,7 @@ sz_status kv_append(const kv_cache* cache, const kv_batch* batch, const kv_appen
  * Scores, softmax statistics and the sum over j are held in 32 bits; the
  * weights are rounded to 16 bits before they multiply the values (BF16 for a
  * BF16 cache, FP16 for an E5M2 one).
+ * d_out may be d_q itself (same stride); other outputs must not overlap inputs.
  * d_workspace: >= kv_attention_workspace_bytes of the same arguments, need
  * not be initialised, clobbered (may be NULL when that is 0). ---- */
 typedef struct {
