@@ -27,33 +27,24 @@ __device__ inline void flag(int32_t* status) {
 
 __device__ inline f32x8 to_f32(u32x4 x) { return __builtin_convertvector(__builtin_bit_cast(bf16x8, x), f32x8); }
 
-// The last s in [0, n) with low(s) <= target, low ascending; 0 where there is
-// none, and some s in [0, n) whatever low gives.  The 64 lanes try 64 places
-// at a time, so that up to 64 sequences cost one trip to memory and 4096 two,
-// where a binary search makes 6 and 12, each waiting for the last.  Every
-// lane of the wave takes part.
+// last_not_above() by a wave, each lane trying one place.  Every lane takes part.
 template <typename Low>
-__device__ inline uint32_t last_not_above(uint32_t n, int64_t target, Low low) {
-    uint32_t from = 0;
-    while (n > 1) {
-        const uint32_t step = (n + 63) / 64, i = sz::lane_id() * step;
-        const uint64_t not_above = __ballot(i < n && low(from + (i < n ? i : 0)) <= target);
-        const uint32_t k = not_above ? 63 - __builtin_clzll(not_above) : 0;
-        from += k * step;
-        n = n - k * step < step ? n - k * step : step;
-    }
-    return uniform(from);
+__device__ inline uint32_t wave_last_not_above(uint32_t n, int64_t target, Low low) {
+    return uniform(last_not_above(n, [&](uint32_t from, uint32_t step, uint32_t left) -> uint64_t {
+        const uint32_t i = sz::lane_id() * step;
+        return __ballot(i < left && low(from + (i < left ? i : 0)) <= target);
+    }));
 }
 
-// seq_of_token() by a wave: where no sequence has the row, some sequence;
-// callers compare t with its span.
+// The sequence that has token row t, cu[s] <= t < cu[s + 1]; where none has,
+// some sequence: callers compare t with its span.
 __device__ inline uint32_t wave_seq_of_token(const Batch& b, uint32_t t) {
-    return last_not_above(b.num_seqs, t, [&](uint32_t s) -> int64_t { return gptr(b.cu)[s]; });
+    return wave_last_not_above(b.num_seqs, t, [&](uint32_t s) -> int64_t { return gptr(b.cu)[s]; });
 }
 
-// tile_of() by a wave.
+// The tile in `slot`, if any.
 __device__ inline Tile wave_tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t group, uint32_t M) {
-    const uint32_t s = last_not_above(b.num_seqs, static_cast<int64_t>(slot), [&](uint32_t i) -> int64_t {
+    const uint32_t s = wave_last_not_above(b.num_seqs, static_cast<int64_t>(slot), [&](uint32_t i) -> int64_t {
         return static_cast<int64_t>(tile_slot(b, i, group, M));
     });
     return tile_in(b, mask, s, slot, group, M);

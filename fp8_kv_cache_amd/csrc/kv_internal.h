@@ -46,17 +46,23 @@ KV_HD Span span_of(const Batch& b, uint32_t s) {
     return p;
 }
 
-// The sequence that has token row t: cu[s] <= t < cu[s + 1], or num_seqs
-// where none has (padding behind the last).  Terminates, and answers inside
-// [0, num_seqs], whatever cu holds; callers compare t with the span found.
-KV_HD uint32_t seq_of_token(const Batch& b, uint32_t t) {
-    uint32_t lo = 0, hi = b.num_seqs;   // the first s with cu[s + 1] > t
-    while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (b.cu[mid + 1] > static_cast<int32_t>(t)) hi = mid;
-        else lo = mid + 1;
+// The last s in [0, n) with low(s) <= target, low ascending; 0 where there is
+// none, and some s in [0, n) whatever low gives.  Up to 64 places are tried at
+// a time: vote(from, step, n) has bit i set where i * step < n and
+// low(from + i * step) <= target, so that a wave finds one of 64 sequences in
+// one trip to memory and one of 4096 in two, where a binary search makes 6
+// and 12, each waiting for the last.
+template <typename Vote>
+KV_HD uint32_t last_not_above(uint32_t n, Vote vote) {
+    uint32_t from = 0;
+    while (n > 1) {
+        const uint32_t step = (n + 63) / 64;
+        const uint64_t not_above = vote(from, step, n);
+        const uint32_t k = not_above ? 63 - __builtin_clzll(not_above) : 0;
+        from += k * step;
+        n = n - k * step < step ? n - k * step : step;
     }
-    return lo;
+    return from;
 }
 
 // Page of a sequence's position p >= 0, or -1: past the table, or not a
@@ -129,16 +135,6 @@ KV_HD Tile tile_in(const Batch& b, const Mask& mask, uint32_t s, uint64_t slot, 
     t.rows = static_cast<uint32_t>(rows - row0 < M ? rows - row0 : M);
     tile_range(t, mask, group);
     return t;
-}
-
-KV_HD Tile tile_of(const Batch& b, const Mask& mask, uint64_t slot, uint32_t group, uint32_t M) {
-    uint32_t lo = 0, hi = b.num_seqs;
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (tile_slot(b, mid, group, M) <= slot) lo = mid;
-        else hi = mid;
-    }
-    return tile_in(b, mask, lo, slot, group, M);
 }
 
 // Splits of a tile's positions: split z has [lo + z * len, lo + (z + 1) * len) of [lo, hi).
