@@ -109,7 +109,8 @@ bool take_attention(const kv_cache* cache, const kv_batch* batch, const kv_atten
     if (empty(a.batch)) return true;
     const uint64_t row = static_cast<uint64_t>(x->q_heads) * a.cache.head_dim;
     if (!usable(x->d_q) || !usable(x->d_out) || (x->d_lse && !aligned(x->d_lse, 4)) ||
-        !stride_ok(x->q_stride, row, a.batch.total_tokens, 2) || !stride_ok(x->out_stride, row, a.batch.total_tokens, 2))
+        !stride_ok(x->q_stride, row, a.batch.total_tokens, 2) || !stride_ok(x->out_stride, row, a.batch.total_tokens, 2) ||
+        (x->d_q == x->d_out && x->q_stride != x->out_stride && a.batch.total_tokens > 1))
         return false;
     a.plan = attention_plan(a.cache, a.batch, a.group, x->window, a.e5m2);
     if (attention_groups(a) >= kMaxGroups) return false;
@@ -235,8 +236,8 @@ kvi::AttentionPlan kvi::attention_plan(const Cache& c, const Batch& b, uint32_t 
     AttentionPlan p{};
     const uint64_t most_rows = static_cast<uint64_t>(b.max_tokens) * group;
     const uint64_t rows = static_cast<uint64_t>(b.total_tokens) * group;
-    // 256 rows share a tile of keys where a sequence has many (2048 new of 8192: 276 us, against 295 with 128), 128
-    // where it has few (100 new of 400, 400 rows: 18 us, 21) and where the registers of a wave fill a SIMD (D = 256).
+    // 256 rows share a tile of keys where a sequence has many (a prompt of 8192: 1240 us, against 1304 with 128), 128
+    // where it has few (100 new of 400, 400 rows: 19 us, 22) and where the registers of a wave fill a SIMD (D = 256).
     p.tile = most_rows <= kFewRows ? kFewRows : most_rows <= 512 || c.head_dim > 128 ? 128 : 256;
     // positions that a tile can see
     uint64_t range = b.max_kv_len;
@@ -254,7 +255,7 @@ kvi::AttentionPlan kvi::attention_plan(const Cache& c, const Batch& b, uint32_t 
         const uint64_t most = range / p.granule + 2;
         if (joins && range > 1024 && static_cast<uint64_t>(b.num_seqs) * c.kv_heads < 4096 && b.num_seqs * most < (uint64_t(1) << 32)) {
             // Two heads a workgroup where their rows are neighbours in a token-major page and there are positions
-            // enough (64 x 1 to 8192 keys: 213 us, against 221; E5M2: 130, 140; but 8 x 1 to 8192: 42, 38).
+            // enough (64 x 1 to 8192 keys: 209 us, against 220; E5M2: 127, 138; but 8 x 1 to 8192: 41, 37).
             const bool neighbours = c.head_stride < c.token_stride && c.kv_heads % 2 == 0;
             p.heads = neighbours && b.num_seqs * range >= 3 << 16 ? 2 : 1;
             p.units = static_cast<uint32_t>(at_once * p.heads / c.kv_heads / 8 * 8);

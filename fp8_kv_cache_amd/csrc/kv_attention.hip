@@ -147,13 +147,22 @@ __device__ inline void add_not_finite(const SZ_GLOBAL uint8_t* from, float* o) {
 
 // How far (powers of two) a row's maximum may pass the one its sums are
 // scaled by before they are rescaled.  FP16 weights lose nothing by it (2 x
-// 1000 of 12345 E5M2 keys: 667 us, 694 without).  BF16 ones do: scaled by the
+// 1000 of 12345 E5M2 keys: 690 us, 725 without).  BF16 ones do: scaled by the
 // maximum itself, the largest weight is 1 and is not rounded, and the error
 // of peaked rows is a quarter smaller (0.0018 of the result's norm at 64 x 1
-// to 8192 keys, 0.0023 with this at 8), which is worth the 4% it takes of
-// long chunks (2048 new of 8192: 289 us, 278) and nothing elsewhere.
+// to 8192 keys, 0.0023 with this at 8), which is worth what it takes of long
+// chunks (2048 new of 8192: 296 us, 293; a prompt of 8192 tokens under 64
+// query heads: 1240, 1167) and nothing elsewhere.
 template <bool kE5M2>
 constexpr float kSlack = kE5M2 ? 8.f : 0.f;
+
+// FP16 weights are 2^kLift times themselves, the sum with them: at most
+// 2^(kSlack + kLift) = 2^15, and those below 2^-14 of a long row's largest
+// keep 7 more of the bits that FP16's small exponents would take (131072 of
+// 2^-25 each, half a step, were all lost against a weight of 1, and with them
+// 2^-8 of the row).
+template <bool kE5M2>
+constexpr float kLift = kE5M2 ? 7.f : 0.f;
 
 // LDS order inside one wave: its LDS instructions execute in order; this
 // keeps the compiler from moving one lane's reads over another's writes.
@@ -293,8 +302,8 @@ struct Few {
     static constexpr uint32_t kKeys = kE5M2 ? 64 : 32;   // a block: 16 KB of K and V either way at D = 128
     static constexpr uint32_t kSize = kE5M2 ? 1 : 2;
     // Rows of whole 128-byte lines are read once and kept in no cache (64 x 1
-    // to 8192 keys: 213 us, against 238 with plain loads); neighbouring heads
-    // share the lines of others (D = 80, 32 x 5 tokens: 108 us plain, 118).
+    // to 8192 keys: 209 us, against 235 with plain loads); neighbouring heads
+    // share the lines of others (D = 80, 32 x 5 tokens: 106 us plain, 117).
     static constexpr bool kOwnLines = D * kSize % 128 == 0;
     // rows in LDS; BF16 V: 8 dwords modulo 16, 16 rows of 32 bytes meet all banks
     static constexpr uint32_t kK = D * kSize + 16, kV = kE5M2 ? D + 16 : 2 * D + (D % 32 ? 0 : 32);
@@ -329,7 +338,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
                                           : u32x4{0, 0, 0, 0};
     float c = a.scale * kLog2e;
     if constexpr (kE5M2) c = to_fp16<kFrags>(q, c, [](float x) { return row_max(x); });
-    c = fmaxf(c, 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
+    c = fminf(fmaxf(c, 1.17549435e-38f), 3.402823466e38f);   // masked scores times c are -Inf and zeros 0, not NaN
 
     f32x4 o[kTiles];
 #pragma unroll
@@ -431,7 +440,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
 #pragma unroll
             for (uint32_t d = 0; d < kTiles; ++d) o[d] *= r;
         }
-        const float base = m == -kInf ? 0.f : m;
+        const float base = m == -kInf ? 0.f : m - kLift<kE5M2>;
         u32x4 p[kSub / 2];
 #pragma unroll
         for (uint32_t kk = 0; kk < kSub / 2; ++kk) {
@@ -481,7 +490,7 @@ __device__ inline void attend_few(const AttentionArgs& a, const Tile& t, uint32_
     KV_LDS float* sums = lds_as<float>((LdsBytes)lds);                                   // [wave][row][D + 4]
     l = row_sum(l);
     __syncthreads();   // the stages have been read
-    if (g == 0) stats[wave * 16 + c16] = f32x2{m, l};
+    if (g == 0) stats[wave * 16 + c16] = f32x2{m - kLift<kE5M2>, l};
 #pragma unroll
     for (uint32_t d = 0; d < kTiles; ++d)
         *(KV_LDS f32x4*)(sums + (wave * 16 + c16) * (D + 4) + 16 * d + 4 * g) = o[d];
@@ -580,10 +589,10 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : few_a_cu(D, kE5M2)) void k_att
 // the work between the products (a wave and tile of 64 keys: 1024 cycles of
 // matrix instructions, about as many of vector ones), which overlaps with the
 // other wave of the SIMD only in part: 2048 new of 8192 keys at D = 128, 32
-// query heads, 276 us in tiles of 256 rows, 871 TFLOP/s of the 1330 that a
+// query heads, 272 us in tiles of 256 rows, 884 TFLOP/s of the 1330 that a
 // large library product reaches here.  Taking turns by barriers (one half of
-// the workgroup multiplies while the other computes weights) measured the
-// same as two workgroups left alone, 298 us.
+// the workgroup multiplies while the other computes weights) was no better
+// than leaving them alone.
 template <uint32_t D>
 constexpr uint32_t kValueRow = ((2 * D + 63) / 64 | 1) * 64;      // V rows: 4 rows of 64 bytes meet all banks
 
@@ -630,7 +639,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
         q[f] = live ? *reinterpret_cast<const SZ_GLOBAL u32x4*>(from + 16 * f + 8 * half) : u32x4{0, 0, 0, 0};
     float c = a.scale * kLog2e;
     if constexpr (kE5M2) c = to_fp16<kFrags>(q, c, [](float x) { return fmaxf(swap32(x, false), swap32(x, true)); });
-    c = fmaxf(c, 1.17549435e-38f);   // stays positive: masked scores times c are -Inf, not NaN
+    c = fminf(fmaxf(c, 1.17549435e-38f), 3.402823466e38f);   // masked scores times c are -Inf and zeros 0, not NaN
 
     f32x16 o[kTiles];
 #pragma unroll
@@ -767,7 +776,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] *= r;
             }
-            const float base = m == -kInf ? 0.f : m;
+            const float base = m == -kInf ? 0.f : m - kLift<kE5M2>;
             auto weights = [&](uint32_t kk) {   // P^T operand of keys 16 kk ..
                 f32x8 e;
 #pragma unroll
@@ -779,7 +788,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
             };
             const LdsBytes values = buffer + N * kKeyRow<D>;
             const LdsBytes read = values + (4 * half + lane % 16 / 4) * kValueRow<D> + c32 / 16 * 32 + lane % 4 * 8;
-            __builtin_amdgcn_s_setprio(1);   // ahead of a wave that is at its scores: 6% at 2048 new of 8192
+            __builtin_amdgcn_s_setprio(1);   // ahead of a wave at its scores (2 x 1000 of 12345: 690 us, 727 without)
 #pragma unroll
             for (uint32_t kk = 0; kk < 2 * kSub; ++kk) {
                 const u32x4 p = weights(kk);
@@ -818,7 +827,7 @@ __global__ __launch_bounds__(64 * W, D <= 128 ? 2 : 1) void k_attend_tile(Attent
     if (__any(table.bad) && lane == 0) flag(a.status);
 
     const float sum = swap32(l, false) + swap32(l, true);
-    const float base = m == -kInf ? 0.f : m;
+    const float base = m == -kInf ? 0.f : m - kLift<kE5M2>;
     if (splits <= 1) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         SZ_GLOBAL uint16_t* to = gptr(a.out) + static_cast<uint64_t>(at.token) * a.out_stride + at.head * D;

@@ -76,8 +76,8 @@ class PageBatch:
     cu_tokens int32 [seqs + 1] (sequence s has the token rows cu[s] ..
     cu[s+1] - 1) and kv_lens int32 [seqs] (cached tokens, the new ones
     among them).  total_tokens is the row count of the step's tensors (rows
-    from cu[-1] on are padding), max_tokens and max_kv_len bound what the
-    device arrays hold; what is not given is read from them, which waits for
+    from cu[-1] on are padding), max_tokens (1 or more) and max_kv_len bound
+    what the device arrays hold; what is not given is read from them, which waits for
     the device.  The arrays may change between calls within those bounds."""
 
     def __init__(self, page_table, cu_tokens, kv_lens, total_tokens=None, max_tokens=None, max_kv_len=None):
@@ -96,7 +96,7 @@ class PageBatch:
         if total_tokens is None:
             total_tokens = int(cu_tokens[-1])
         if max_tokens is None:
-            max_tokens = int((cu_tokens[1:] - cu_tokens[:-1]).max()) if seqs else 0
+            max_tokens = max(1, int((cu_tokens[1:] - cu_tokens[:-1]).max())) if seqs else 0
         if max_kv_len is None:
             max_kv_len = int(kv_lens.max()) if seqs else 0
         for n in (total_tokens, max_tokens, max_kv_len):

@@ -78,7 +78,7 @@ typedef struct {
     uint32_t pages_per_seq;      /* >= 1 */
     uint32_t num_seqs;           /* < 2^20 */
     uint32_t total_tokens;       /* rows of the per-token tensors, < 2^24 */
-    uint32_t max_tokens;         /* no n_s is larger */
+    uint32_t max_tokens;         /* >= 1; no n_s is larger */
     uint32_t max_kv_len;         /* no kv_len_s is larger; < 2^31 - 2^17 */
     uint32_t reserved;           /* must be 0 */
 } kv_batch;
@@ -153,8 +153,8 @@ typedef struct {
 
 /* A call whose launch would have too many workgroups is refused: the rows of
  * a KV head, total_tokens * q_heads / kv_heads, make tiles of 16 (where
- * max_tokens * q_heads / kv_heads <= 16: one a sequence) or 128 rows, and
- * tiles * kv_heads stays below 2^23. */
+ * max_tokens * q_heads / kv_heads <= 16: one a sequence), or of 128 or 256
+ * rows, and tiles * kv_heads stays below 2^23. */
 
 /* Depends on the shapes and limits in the descriptors alone.  Pure host
  * function; 0 for arguments that kv_attention refuses. */

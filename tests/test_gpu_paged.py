@@ -851,3 +851,63 @@ def test_two_graphs_and_eager_work_side_by_side(paged):
         eager = paged.attention(cache, batch, qs[0])
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, want[0])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_small_weights_of_a_long_row_are_not_lost(paged, new):
+    """E5M2: one key at weight 1 and all others at 2^-25.3, values 0 and 1, so
+    that the result is the small weights' sum n w / (1 + n w).  Lifted by 2^7
+    a weight is 2^-18.3 and FP16's step there 2^-24: half a step is 2^-6.7 of
+    it.  The output's rounding adds 2^-8, the score's 32-bit roundings (a
+    product of 25.3 and a difference of that size) less than 2^-18, and the
+    sum's n 2^-24 of it 2^-9."""
+    say("small weights", new)
+    kv = 30000
+    st = Setup([new], [kv], 1, 64, E5M2)
+    for pool, fill in ((st.k, 0.0), (st.v, 1.0)):
+        pool[st.table[0].long()] = torch.tensor(fill).to(st.k.dtype)
+    page, slot = st.place(0, 5)
+    st.k[page, slot, 0, 0] = torch.tensor(16.0).to(st.k.dtype)
+    st.v[page, slot] = torch.zeros(1, 64).to(st.v.dtype)
+    q = torch.zeros(new, 2, 64, dtype=torch.bfloat16)
+    q[:, :, 0] = 1
+    cache, batch, status = handles(paged, st)
+    out, lse = paged.attention(cache, batch, q.cuda(), scale=25.3 * math.log(2) / 16, return_lse=True, status=status)
+    n = kv - new + torch.arange(new, dtype=torch.float64)[:, None, None]   # keys beside the one
+    tail = n * 2.0 ** -25.3
+    want = tail / (1 + tail)
+    off = (out.cpu().double() - want).abs() / want
+    assert float(off.max()) <= 2.0 ** -6.7 + 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -17
+    want_lse = 25.3 * math.log(2) + torch.log1p(tail[..., 0])
+    # n 2^-24 of the sum, and the score's and the logarithm's roundings near 17.5
+    assert ((lse.cpu().double() - want_lse).abs() <= kv * 2.0 ** -24 + 17.6 * 2.0 ** -22).all() and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("new", [1, 40])
+def test_the_largest_scale(paged, new, dtype):
+    """Scores of 0 stay 0 at any scale: every row is the mean of its values,
+    and keys that a row does not see stay out."""
+    say("largest scale", new, dtype)
+    st = Setup([new], [new + 30], 1, 64, dtype)
+    st.k[st.table[0].long()] = torch.tensor(0.0).to(st.k.dtype)
+    check_attention(paged, st, 2, scale=3.4e38)
+
+
+@pytest.mark.parametrize("kv", [40, 3000])
+def test_a_step_without_new_tokens(paged, kv):
+    """Sequences without new tokens, and rows of padding: nothing is written."""
+    say("no new tokens", kv)
+    st = Setup([0, 0], [kv, 7], 2, 64, BF16, pad=3)
+    cache = paged.PagedCache(up(st.k), up(st.v))
+    batch = paged.PageBatch(st.table.cuda(), st.cu.cuda(), st.kv_lens.cuda(), 3)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, x = marked((3, 4, 64)), st.rows(2).cuda()
+    paged.attention(cache, batch, st.rows(4).cuda(), out=out, status=status)
+    k, v = paged.gather(cache, batch, marked((3, 2, 64)), marked((3, 2, 64)), status=status)
+    paged.append(cache, batch, x, x, status=status)
+    paged.scatter(cache, batch, x, x, status=status)
+    for y in (out, k, v):
+        assert (y.view(torch.uint8) == MARK).all()
+    assert torch.equal(bits(down(cache.k)), bits(st.k)) and torch.equal(bits(down(cache.v)), bits(st.v))
+    assert int(status) == 0

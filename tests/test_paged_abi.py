@@ -208,3 +208,16 @@ def test_library_is_one_and_device_code_has_no_packed_fp32(sz):
         instructions = [ln.split()[0] for ln in r.stdout.splitlines() if re.match(r"\s+[sv]_\w+", ln)]
         assert not [i for i in instructions if i in ("v_pk_add_f32", "v_pk_mul_f32", "v_pk_fma_f32")]
         assert any(i.startswith("v_mfma") for i in instructions) == (name == "kv_attention.hip")
+
+
+def test_attention_in_place_wants_one_stride(sz):
+    """A row written into the query's place must not be another row's query."""
+    for strides in (dict(q_stride=8192), dict(out_stride=8192)):
+        a = attention_args(sz, **strides)
+        assert sz.kv_attention(cache(sz), batch(sz), a, FAKE, 1 << 40, stream=0) == sz.SZ_ERR_INVALID_ARGUMENT
+        assert sz.kv_attention_workspace_bytes(cache(sz), batch(sz), a) == 0
+    apart = attention_args(sz, d_out=FAKE + (1 << 20), out_stride=8192)
+    long = batch(sz, num_seqs=1, total_tokens=1, max_tokens=1, max_kv_len=100000, pages_per_seq=7000, pages_stride=7000)
+    assert sz.kv_attention_workspace_bytes(cache(sz), long, apart) > 0
+    # one token has one row, whatever its stride
+    assert sz.kv_attention_workspace_bytes(cache(sz), long, attention_args(sz, out_stride=8192)) > 0
