@@ -589,7 +589,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : few_a_cu(D, kE5M2)) void k_att
 // the work between the products (a wave and tile of 64 keys: 1024 cycles of
 // matrix instructions, about as many of vector ones), which overlaps with the
 // other wave of the SIMD only in part: 2048 new of 8192 keys at D = 128, 32
-// query heads, 272 us in tiles of 256 rows, 884 TFLOP/s of the 1330 that a
+// query heads, 275 us in tiles of 256 rows, 875 TFLOP/s of the 1330 that a
 // large library product reaches here.  Taking turns by barriers (one half of
 // the workgroup multiplies while the other computes weights) was no better
 // than leaving them alone.

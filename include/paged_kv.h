@@ -17,10 +17,11 @@
  *   num_seqs sequences with n_s new tokens each, packed: sequence s has the
  *   rows cu[s] .. cu[s+1] - 1 of every per-token tensor (cu[0] >= 0,
  *   ascending, cu[num_seqs] <= total_tokens; rows that no sequence has are
- *   padding and are left as they were).  kv_len_s counts the sequence's tokens with the new ones, so new
- *   token i has position p = kv_len_s - n_s + i.  A token with p < 0 has no
- *   place: append and scatter drop it, gather gives zeros, its attention row
- *   is empty.  The same descriptor serves all four calls.
+ *   padding and are left as they were).  kv_len_s counts the sequence's
+ *   tokens with the new ones, so new token i has position
+ *   p = kv_len_s - n_s + i.  A token with p < 0 has no place: append and
+ *   scatter drop it, gather gives zeros, its attention row is empty.  The
+ *   same descriptor serves all four calls.
  *
  *   Tables and lengths are device data, so the host cannot check them: the
  *   kernels do.  A page id outside [0, num_pages) or past pages_per_seq, a
@@ -94,7 +95,7 @@ typedef struct {
  *     pair i = (y_i, y_{i + rotary_dim/2}), or (y_{2i}, y_{2i+1}) if interleaved,
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * and is rounded once, to the cache's dtype (k) or BF16 (q), to nearest
- * even; E5M2 does not saturate (61440 and more give Inf).  Values take no
+ * even (x^2 and their mean are held in 32 bits, with their range); E5M2 does not saturate (61440 and more give Inf).  Values take no
  * norm and no rotation.  A BF16 key without norm and rotation, and a BF16
  * value, is copied bit for bit.  A position at or past max_positions is
  * treated like a bad page: nothing of that token is written, and *d_status
